@@ -70,7 +70,8 @@ enum {
     PA_DEV_BAD_BLOCK = 2,     /* pa_decode: table entry outside [0, NB) (read as zeros) */
     PA_DEV_WAIT_TIMEOUT = 4,  /* a pipeline wait gave up after its bound; output invalid */
     PA_DEV_BAD_CONTEXT = 8,   /* pa_decode: context_lens[s] < 0, > max_ctx or > MB * bs (clamped) */
-    PA_DEV_BAD_PIECES = 16    /* pa_decode merge: inconsistent split records (rows left unwritten) */
+    PA_DEV_BAD_PIECES = 16,   /* pa_decode merge: inconsistent split records (rows left unwritten) */
+    PA_DEV_BAD_POSITION = 32  /* pa_norm_rope_append: position outside the table, token skipped */
 };
 /* Bits 16-23 of the device word, when PA_DEV_WAIT_TIMEOUT is set: which wait
  * gave up last (diagnostics; decode: 1 stage-free, 2 stage-full,
@@ -124,6 +125,53 @@ pa_status pa_reshape_and_cache(const void* key, const void* value, pa_dtype in_d
                                void* key_cache, void* value_cache, pa_dtype cache_dt,
                                const int64_t* slot_mapping, int T, int Hkv, int D, int bs,
                                int64_t NB, float k_scale, float v_scale, pa_stream_t stream);
+
+/*
+ * Norm of every query and key head, rotation by position, and cache append in
+ * one pass: what a layer does between its projections and pa_decode_* /
+ * pa_prefill_*.  (The pages have no counterpart: their step starts at the
+ * append.)  For every t < T and head row x of D elements:
+ *
+ *   y = x * (w + weight_offset) / sqrt(mean(x^2) + eps)   q and k rows, where
+ *       q_weight / k_weight is not NULL (else y = x)
+ *   (a, b) -> (a * cos - b * sin, b * cos + a * sin)      the rot_dim / 2 pairs
+ *       of q and k rows: elements (j, j + rot_dim / 2), or with interleaved
+ *       != 0 (2j, 2j + 1); cos = cos_sin[p, j], sin = cos_sin[p, rot_dim / 2 + j]
+ *       with p = positions[t].  Elements from rot_dim on are not rotated.
+ *   q_out[t, h, :] = the q row; the k row and the unchanged v row go to slot
+ *       slot_mapping[t] of key_cache / value_cache, as pa_reshape_and_cache
+ *       writes them (fp8: y / k_scale, v / v_scale to nearest even, saturating).
+ *
+ * All arithmetic is fp32 and each result is rounded once, to nearest even.
+ *
+ *   q, q_out     [T, Hq, D] of in_dt (F32, F16, BF16): D contiguous, heads D
+ *                apart, tokens q_stride / q_out_stride ELEMENTS apart (so the
+ *                three inputs may be slices of one [T, (Hq + 2 Hkv) * D]
+ *                projection output).  q_out may be q itself; any other
+ *                overlap of an output with an input is undefined.
+ *   k, v         [T, Hkv, D], strides k_stride, v_stride likewise.
+ *   q_weight, k_weight   device [D] of in_dt, or NULL.
+ *   cos_sin      device fp32 [table_rows, rot_dim]; positions device int64 [T].
+ *                Both may be NULL with rot_dim == 0 (no rotation).
+ *   rot_dim      a multiple of 16 in [0, D]; D in {64, 128, 256}.
+ *   slot_mapping device int64 [T]; < 0: nothing is written to the cache for the
+ *                token (its q row is).  Slots of one call are distinct, else
+ *                one of the tokens wins.  A slot >= NB * bs writes no cache row
+ *                and sets PA_DEV_BAD_SLOT.
+ * A position outside [0, table_rows) skips the token (q row included) and sets
+ * PA_DEV_BAD_POSITION.  cache_dt == in_dt or PA_FP8_E4M3; scales as in
+ * pa_reshape_and_cache.  Strides are multiples of 16 bytes, pointers 16-byte
+ * aligned.  T == 0 is a no-op.
+ */
+pa_status pa_norm_rope_append(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              pa_dtype in_dt, const void* q_weight, const void* k_weight,
+                              float eps, float weight_offset, const float* cos_sin,
+                              int64_t table_rows, const int64_t* positions, int rot_dim,
+                              int interleaved, void* key_cache, void* value_cache,
+                              pa_dtype cache_dt, const int64_t* slot_mapping, int T, int Hq,
+                              int Hkv, int D, int bs, int64_t NB, float k_scale, float v_scale,
+                              pa_stream_t stream);
 
 /*
  * Copy-on-write block copy -- intelliparadigm PagedAttention article §3.3
@@ -199,6 +247,39 @@ pa_status pa_decode(void* out, const void* q, pa_dtype q_dt,
                     int S, int Hq, int Hkv, int D, int bs, int64_t NB, int max_ctx,
                     float scale, float k_scale, float v_scale, int partition,
                     void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_decode with modified scores and masks: layers whose scores are capped by a
+ * tanh, get a bias that grows with the distance, or see a sliding window or
+ * only their own document.  (The pages have no counterpart.)  The query of
+ * sequence s sits at position p = n - 1 (n = context_lens[s]); for key i
+ *
+ *   z_i = scale * <q[s, h, :], k_i>
+ *   z_i = softcap * tanh(z_i / softcap)          softcap > 0 (0: none)
+ *   z_i = z_i - slopes[h] * (p - i)              slopes not NULL, fp32 [Hq]
+ *   out[s, h, :] = sum_i softmax(z)_i v_i over the visible keys, those with
+ *       p - i < window                           window > 0 (0: no window)
+ *       i >= key_start[s]                        key_start not NULL, int32 [S]
+ *
+ * A sequence with no visible key (or n == 0) gives a zero row.  Blocks that
+ * hold no visible key are not read, and their table entries may be anything;
+ * keys and values that are not visible reach nothing, whatever they hold.
+ *
+ * Arguments, dtypes, shapes, errors and memory otherwise as pa_decode, except:
+ * partition >= 0 (no balanced grid), its partitions counted from the block of
+ * the first visible key; workspace of pa_decode_scored_workspace_size() bytes.
+ * With a window, pa_decode_suggest_partition takes the lengths cut to it.
+ */
+pa_status pa_decode_scored_workspace_size(int S, int Hq, int D, int bs, int max_ctx, int window,
+                                          int partition, size_t* bytes);
+pa_status pa_decode_scored(void* out, const void* q, pa_dtype q_dt, const void* key_cache,
+                           const void* value_cache, pa_dtype cache_dt,
+                           const int32_t* block_tables, int MB, const int32_t* context_lens,
+                           int S, int Hq, int Hkv, int D, int bs, int64_t NB, int max_ctx,
+                           float scale, float k_scale, float v_scale, float softcap,
+                           const float* slopes, int window, const int32_t* key_start,
+                           int partition, void* workspace, size_t workspace_bytes,
+                           pa_stream_t stream);
 
 /*
  * pa_decode without a caller-provided workspace.  (The pages have no

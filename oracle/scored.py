@@ -1,0 +1,128 @@
+"""The fused norm / rotation / append and the attentions with modified scores, in 64 bits.
+
+Plain statements from the formulas in include/pa.h, on CPU torch tensors in float64.
+They share no code with the CUDA library.  Every attention result comes with the
+two sums its error bound needs (see ``Bound``).
+"""
+from __future__ import annotations
+
+import dataclasses
+import math
+from typing import Optional
+
+import torch
+
+
+def stored(x: torch.Tensor) -> torch.Tensor:
+    """The values a tensor of any storage dtype holds, in float64."""
+    return x.float().double() if x.dtype == torch.float8_e4m3fn else x.double()
+
+
+# ----------------------------------------------------------- norm, rotation, append
+
+def norm_rope(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float, weight_offset: float,
+              cos_sin: Optional[torch.Tensor], positions, interleaved: bool):
+    """x [T, H, D] -> (rows in float64, the magnitude |a| + |b| each element is made of)."""
+    y = stored(x)
+    if weight is not None:
+        rms = torch.sqrt((y * y).mean(-1, keepdim=True) + eps)
+        y = y / rms * (stored(weight) + weight_offset)
+    size = y.abs()
+    if cos_sin is None or cos_sin.shape[1] == 0:
+        return y, size
+    out, osize = y.clone(), size.clone()
+    r = cos_sin.shape[1]
+    for j in range(r // 2):
+        ia, ib = (2 * j, 2 * j + 1) if interleaved else (j, j + r // 2)
+        c = cos_sin[positions, j].double()[:, None]
+        s = cos_sin[positions, r // 2 + j].double()[:, None]
+        a, b = y[..., ia], y[..., ib]
+        out[..., ia], out[..., ib] = a * c - b * s, b * c + a * s
+        osize[..., ia] = osize[..., ib] = size[..., ia] + size[..., ib]
+    return out, osize
+
+
+# ------------------------------------------------------------------------- attention
+
+@dataclasses.dataclass
+class Bound:
+    """out: the result; weighted: sum_i p_i |v_i| per output element; score: a
+    bound on how large the terms of one score get (sum_d |q_d k_d| * scale, the
+    cap, the bias), per output row."""
+    out: torch.Tensor
+    weighted: torch.Tensor
+    score: torch.Tensor
+
+    def tolerance(self, out_dtype: torch.dtype, p_dtype: Optional[torch.dtype], D: int):
+        """How far a kernel may be off: the output's own rounding, the rounding
+        of each probability to p_dtype (in the numerator and in the sum), and the
+        fp32 arithmetic of the scores: D products and the modifications, each
+        within 2^-24 of the largest term, which move every probability by the
+        same relative amount; the weighted sum in fp32."""
+        half = lambda t: torch.finfo(t).eps / 2                          # noqa: E731
+        up = half(p_dtype) if p_dtype is not None else 0.0
+        dz = (D + 32) * 2.0 ** -24 * (1 + self.score)
+        rel = 2 * up + 2 * dz + 2.0 ** -18
+        return half(out_dtype) * self.out.abs() + rel[..., None] * self.weighted + 1e-30
+
+
+def scored_attention(q, key_cache, value_cache, block_tables, context_lens, query_start, scale,
+                     softcap=0.0, slopes=None, window=0, key_start=None, prefix_lens=None,
+                     k_scale=1.0, v_scale=1.0) -> Bound:
+    """q [T, Hq, D]; query_start [S + 1] (None: one new token per sequence)."""
+    T, Hq, D = q.shape
+    NB, bs, Hkv, _ = key_cache.shape
+    G = Hq // Hkv
+    S = len(context_lens)
+    qs = list(range(S + 1)) if query_start is None else [int(x) for x in query_start]
+    out = torch.zeros(T, Hq, D, dtype=torch.float64)
+    wtd, big = torch.zeros_like(out), torch.zeros(T, Hq, dtype=torch.float64)
+    qd = stored(q)
+    for s in range(S):
+        a, b, n = qs[s], qs[s + 1], int(context_lens[s])
+        L = b - a
+        if L == 0:
+            continue
+        p = torch.arange(n - L, n)[:, None]
+        i = torch.arange(n)[None, :]
+        ahead = p if prefix_lens is None else torch.clamp(p, min=int(prefix_lens[s]) - 1)
+        seen = i <= ahead
+        if window:
+            seen &= p - i < window
+        if key_start is not None:
+            ks = key_start[s:s + 1] if query_start is None else key_start[a:b]
+            seen &= i >= ks[:, None]
+        if not seen.any():
+            continue
+        # rows of keys nobody sees are left out: their blocks need not exist
+        keys = torch.nonzero(seen.any(0))[:, 0]
+        seen = seen[:, keys]
+        dist = (p - keys[None, :]).abs().double()
+        blk, off = block_tables[s][keys // bs].long(), keys % bs
+        kk = stored(key_cache[blk, off]) * k_scale          # [n', Hkv, D]
+        vv = stored(value_cache[blk, off]) * v_scale
+        for h in range(Hq):
+            z = scale * (qd[a:b, h] @ kk[:, h // G].T)
+            size = scale * (qd[a:b, h].abs() @ torch.nan_to_num(kk[:, h // G]).abs().T)
+            if softcap:
+                z = softcap * torch.tanh(z / softcap)
+                size = size + softcap
+            if slopes is not None:
+                z = z - float(slopes[h]) * dist
+                size = size + abs(float(slopes[h])) * dist
+            z = z.masked_fill(~seen, -math.inf)
+            some = seen.any(1)
+            w = torch.zeros_like(z)
+            w[some] = torch.softmax(z[some], -1)
+            v = vv[:, h // G]
+            bad = ~torch.isfinite(v)
+            if bad.any():      # a value reaches the rows that see its key, and no other
+                fine = w @ torch.where(bad, 0.0, v)
+                for key, d in torch.nonzero(bad).tolist():
+                    fine[seen[:, key], d] += v[key, d]
+                out[a:b, h] = fine
+            else:
+                out[a:b, h] = w @ v
+            wtd[a:b, h] = w @ torch.nan_to_num(v, 0.0, 0.0, 0.0).abs()
+            big[a:b, h] = torch.where(seen, size, 0.0).amax(1)
+    return Bound(out, wtd, big)

@@ -20,11 +20,13 @@ import torch
 
 __all__ = [
     "PaError", "lib", "pa_version", "pa_launch_count", "pa_last_error", "pa_device_status",
-    "pa_reshape_and_cache", "pa_copy_blocks", "pa_decode", "pa_decode_workspace_size",
+    "pa_reshape_and_cache", "pa_norm_rope_append", "pa_copy_blocks", "pa_decode", "pa_decode_workspace_size",
     "pa_decode_suggest_partition", "pa_decode_partition_group", "pa_decode_select", "pa_decode_noalloc", "pa_prefill",
+    "pa_decode_scored", "pa_decode_scored_workspace_size",
     "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_size",
     "BlockPool", "pa_plan_shards",
     "PA_DEV_BAD_SLOT", "PA_DEV_BAD_BLOCK", "PA_DEV_WAIT_TIMEOUT", "PA_DEV_BAD_CONTEXT",
+    "PA_DEV_BAD_POSITION",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -37,6 +39,7 @@ STATUS = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED",
 PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3 = 0, 1, 2, 3
 PA_DEV_BAD_SLOT, PA_DEV_BAD_BLOCK, PA_DEV_WAIT_TIMEOUT, PA_DEV_BAD_CONTEXT = 1, 2, 4, 8
 PA_DEV_BAD_PIECES = 16
+PA_DEV_BAD_POSITION = 32
 
 _TORCH_DT = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16,
              torch.float8_e4m3fn: PA_FP8_E4M3, torch.uint8: PA_FP8_E4M3}
@@ -74,12 +77,17 @@ def lib() -> ctypes.CDLL:
         "pa_launch_count": ([], ctypes.c_uint64),
         "pa_device_status": ([ctypes.POINTER(ctypes.c_uint), I, P], I),
         "pa_reshape_and_cache": ([P, P, I, P, P, I, P, I, I, I, I, I64, F, F, P], I),
+        "pa_norm_rope_append": ([P, I64, P, I64, P, I64, P, I64, I, P, P, F, F, P, I64, P, I, I, P,
+                                 P, I, P, I, I, I, I, I, I64, F, F, P], I),
         "pa_copy_blocks": ([P, P, SZ, I64, P, I, P], I),
         "pa_decode_workspace_size": ([I, I, I, I, I, ctypes.POINTER(SZ)], I),
         "pa_decode_suggest_partition": ([I, I, I, P, ctypes.POINTER(I)], I),
         "pa_decode_partition_group": ([I, I, I, I, I, I, I, I, I, I, ctypes.POINTER(I)], I),
         "pa_decode_select": ([I], I),
         "pa_decode": ([P, P, I, P, P, I, P, I, P, I, I, I, I, I, I64, I, F, F, F, I, P, SZ, P], I),
+        "pa_decode_scored_workspace_size": ([I, I, I, I, I, I, I, ctypes.POINTER(SZ)], I),
+        "pa_decode_scored": ([P, P, I, P, P, I, P, I, P, I, I, I, I, I, I64, I, F, F, F, F, P, I,
+                              P, I, P, SZ, P], I),
         "pa_decode_noalloc": ([P, P, I, P, P, I, P, I, P, I, I, I, I, I, I64, I, F, F, F, I, P], I),
         "pa_prefill": ([P, P, I, P, P, I, P, I, P, P, I, I, I, I, I, I, I64, I, F, P], I),
         "pa_decode_shared_prefix_workspace_size": ([I, I, I, I, I, I, I, I, ctypes.POINTER(SZ)], I),
@@ -186,6 +194,73 @@ def pa_reshape_and_cache(key: torch.Tensor, value: torch.Tensor, key_cache: torc
                                       _stream(stream)))
 
 
+def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
+    """The work is enqueued on the current device's stream: every tensor must
+    live there (a None is skipped)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise PaError(1, f"tensors must be on the current CUDA device (got {t.device})")
+
+
+def _rows(t: torch.Tensor, shape, what: str) -> int:
+    """The stride between tokens of a [T, H, D] tensor whose heads are packed."""
+    if tuple(t.shape) != shape:
+        raise PaError(1, f"{what} must have shape {list(shape)}, got {list(t.shape)}")
+    T, H, D = shape
+    s = t.stride()
+    if (s[2] != 1 and D > 1) or (s[1] != D and H > 1):
+        raise PaError(1, f"the heads of a token of {what} must be contiguous")
+    return s[0] if T > 1 else H * D
+
+
+def pa_norm_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                        eps: float, cos_sin: Optional[torch.Tensor],
+                        positions: Optional[torch.Tensor], key_cache: torch.Tensor,
+                        value_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                        interleaved: bool = False, weight_offset: float = 0.0,
+                        k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """Norm (weights given) and rotate (cos_sin given) every q and k head, write
+    q to q_out and k, v to their cache slots.  q_out/q [T, Hq, D], k/v [T, Hkv, D]:
+    any token stride, so slices of one projection output fit, and q_out may be q.
+    q_weight/k_weight [D]; cos_sin fp32 [rows, rot_dim] (cosines, then sines);
+    positions [T] int64; caches [NB, bs, Hkv, D]; slot_mapping [T] int64."""
+    T, Hq, D = q.shape
+    NB, bs, Hkv, _ = key_cache.shape
+    kv = (T, Hkv, D)
+    strides = (_rows(q_out, (T, Hq, D), "q_out"), _rows(q, (T, Hq, D), "q"), _rows(k, kv, "k"),
+               _rows(v, kv, "v"))
+    in_dt = q.dtype
+    if not (q_out.dtype == k.dtype == v.dtype == in_dt):
+        raise PaError(1, "q_out, q, k and v must have one dtype")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != in_dt or w.numel() != D):
+            raise PaError(1, "a norm weight holds D values of the inputs' dtype")
+    if (key_cache.shape != value_cache.shape or key_cache.dtype != value_cache.dtype
+            or key_cache.shape[3] != D):
+        raise PaError(1, "the caches must be [NB, bs, Hkv, D] of one dtype")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
+        raise PaError(1, "slot_mapping must hold T int64 slots")
+    rows = rot = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+            raise PaError(1, "cos_sin must be float32 [rows, rot_dim]")
+        if positions is None or positions.dtype != torch.int64 or positions.numel() != T:
+            raise PaError(1, "positions must hold T int64 positions")
+        rows, rot = cos_sin.shape
+    else:
+        positions = None
+    _on_current_device(q_out, q, k, v, q_weight, k_weight, cos_sin, positions, key_cache,
+                       value_cache, slot_mapping)
+    _check(lib().pa_norm_rope_append(
+        q_out.data_ptr(), strides[0], q.data_ptr(), strides[1], k.data_ptr(), strides[2],
+        v.data_ptr(), strides[3], _dt(q), _ptr(q_weight), _ptr(k_weight), eps, weight_offset,
+        _ptr(cos_sin), rows, _ptr(positions), rot, 1 if interleaved else 0, _ptr(key_cache),
+        _ptr(value_cache), _dt(key_cache), _ptr(slot_mapping), T, Hq, Hkv, D, bs, NB, k_scale,
+        v_scale, _stream(stream)))
+
+
 def pa_copy_blocks(key_cache: torch.Tensor, value_cache: torch.Tensor, pairs,
                    stream=None) -> None:
     """pairs: host [n, 2] int32 (src, dst) -- a CPU tensor, array or list of pairs."""
@@ -264,6 +339,56 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, key_cache: torch.Tensor,
                            Hkv, D, bs, NB, int(max_ctx), float(scale), float(k_scale),
                            float(v_scale), int(partition), _ptr(workspace), ws_bytes,
                            _stream(stream)))
+
+
+def _attention_args(out, q, key_cache, value_cache, block_tables, context_lens, slopes):
+    """The shape and dtype rules of the modified-score attentions' tensors."""
+    if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype:
+        raise PaError(1, "out and q must be [rows, Hq, D] of one dtype")
+    if (key_cache.dim() != 4 or key_cache.shape != value_cache.shape
+            or key_cache.dtype != value_cache.dtype or key_cache.shape[3] != q.shape[2]):
+        raise PaError(1, "the caches must be [NB, bs, Hkv, D] of one dtype")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise PaError(1, "block_tables and context_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != context_lens.numel():
+        raise PaError(1, "block_tables must be [S, MB]")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != q.shape[1]):
+        raise PaError(1, "slopes must hold Hq float32 values")
+
+
+def pa_decode_scored_workspace_size(S: int, Hq: int, D: int, bs: int, max_ctx: int, window: int,
+                                    partition: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().pa_decode_scored_workspace_size(S, Hq, D, bs, max_ctx, window, partition,
+                                                 ctypes.byref(n)))
+    return n.value
+
+
+def pa_decode_scored(out: torch.Tensor, q: torch.Tensor, key_cache: torch.Tensor,
+                     value_cache: torch.Tensor, block_tables: torch.Tensor,
+                     context_lens: torch.Tensor, max_ctx: int, scale: float,
+                     softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                     window: int = 0, key_start: Optional[torch.Tensor] = None,
+                     k_scale: float = 1.0, v_scale: float = 1.0, partition: int = 0,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """pa_decode with modified scores: softcap (tanh cap, 0: none), slopes (fp32
+    [Hq], distance bias), window (last keys visible, 0: all), key_start (int32
+    [S], first visible key).  workspace: pa_decode_scored_workspace_size()."""
+    _attention_args(out, q, key_cache, value_cache, block_tables, context_lens, slopes)
+    S, Hq, D = q.shape
+    NB, bs, Hkv, _ = key_cache.shape
+    if context_lens.numel() != S:
+        raise PaError(1, "context_lens must hold S lengths")
+    if key_start is not None and (key_start.dtype != torch.int32 or key_start.numel() != S):
+        raise PaError(1, "key_start must hold S int32 positions")
+    _on_current_device(out, q, key_cache, value_cache, block_tables, context_lens, slopes,
+                       key_start, workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().pa_decode_scored(
+        _ptr(out), _ptr(q), _dt(q), _ptr(key_cache), _ptr(value_cache), _dt(key_cache),
+        _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), S, Hq, Hkv, D, bs, NB,
+        max_ctx, scale, k_scale, v_scale, softcap, _ptr(slopes), window, _ptr(key_start),
+        partition, _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def pa_decode_noalloc(out: torch.Tensor, q: torch.Tensor, key_cache: torch.Tensor,

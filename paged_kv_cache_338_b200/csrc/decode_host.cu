@@ -135,6 +135,13 @@ int64_t parts_for(int max_ctx, int partition) {
     return ((int64_t)max_ctx + partition - 1) / partition;
 }
 
+// Tokens a sequence's stages cover with a window: the window and the rest of
+// the stage (one block) its first token lies in.
+int scored_span(int max_ctx, int window, int bs) {
+    if (window <= 0 || window >= max_ctx) return max_ctx;
+    return (int)std::min<int64_t>(max_ctx, (int64_t)window + bs - 1);
+}
+
 bool is_pow2_group(int g) { return g == 1 || g == 2 || g == 4 || g == 8 || g == 16; }
 
 // The shape and dtype rules every decode launch obeys (pa_decode and the
@@ -263,7 +270,7 @@ pa_status pa::decode_impl(void* out, const void* q, pa_dtype q_dt, const void* k
                           int bs, int64_t NB, int max_ctx, float scale, float k_scale,
                           float v_scale, int partition, void* workspace, size_t workspace_bytes,
                           pa_stream_t stream, int prefix_parts, int force_ws,
-                          int fuse_prefix_blocks) {
+                          int fuse_prefix_blocks, const ScoreOpts* mod) {
     pa_status chk = check_decode_shape(q_dt, cache_dt, S, Hq, Hkv, D, bs, max_ctx, partition);
     if (chk) return chk;
     if (MB < 0 || NB <= 0) return fail(PA_ERR_INVALID_ARG, "negative or zero size");
@@ -283,6 +290,11 @@ pa_status pa::decode_impl(void* out, const void* q, pa_dtype q_dt, const void* k
         return fail(PA_ERR_INVALID_ARG, "caches, q and out must be 16-byte aligned");
     if (MB == 0 && max_ctx > 0) return fail(PA_ERR_INVALID_ARG, "MB == 0 with max_ctx > 0");
 
+    // modified scores: only the tokens from the first visible key's stage on
+    // are read, at most the window and the rest of its first stage
+    const bool ranged = mod && (mod->window > 0 || mod->key_start);
+    const int span = mod ? scored_span(max_ctx, mod->window, bs) : max_ctx;
+
     // shared-prefix decode: records up to partition prefix_parts exist even
     // when max_ctx ends inside the prefix (irregular sequences write them)
     const bool fuse = fuse_prefix_blocks > 0;
@@ -290,7 +302,7 @@ pa_status pa::decode_impl(void* out, const void* q, pa_dtype q_dt, const void* k
                               : fuse ? prefix_parts            // the prefix records only
                               : prefix_parts > 0
                                   ? std::max<int64_t>(parts_for(max_ctx, partition), prefix_parts + 1)
-                                  : parts_for(max_ctx, partition);
+                                  : parts_for(span, partition);
     if (max_parts > 65535 || (int64_t)Hkv * G > 65535)
         return fail(PA_ERR_UNSUPPORTED, "too many partitions or heads for the grid");
     // the suffix pass merges its warps' states and the prefix records with
@@ -309,8 +321,10 @@ pa_status pa::decode_impl(void* out, const void* q, pa_dtype q_dt, const void* k
     const bool items = fuse && (sel & 16);
     // 8-token blocks go two to a stage (16 tokens) in the partition kernel,
     // where partitions are whole stages
+    // (with a first visible key one block to a stage, so that no block before
+    // its own is fetched: its table entry may name no block any more)
     const bool pair = bs == 8 && !balanced && !fuse && prefix_parts == 0 && !force_ws &&
-                      partition % 16 == 0;
+                      partition % 16 == 0 && !ranged;
     const int stage_tokens = pair ? 16 : bs;
     // four neighbouring kv heads per CTA (one per consumer warp), read by one
     // tensor-map copy per block and segment, where a stage of the four heads'
@@ -334,7 +348,7 @@ pa_status pa::decode_impl(void* out, const void* q, pa_dtype q_dt, const void* k
     size_t need = 0;
     if (balanced) need = balanced_bytes(S, Hq, D, gc);
     else if (force_ws || fuse) need = (size_t)S * Hq * max_parts * (sizeof(float) * 2 + sizeof(float) * D);
-    else pa_decode_workspace_size(S, Hq, D, max_ctx, partition, &need);
+    else pa_decode_workspace_size(S, Hq, D, span, partition, &need);
     if (force_ws && balanced) return fail(PA_ERR_INVALID_ARG, "the balanced grid has no prefix mode");
     if (need && (!workspace || workspace_bytes < need || !aligned16(workspace)))
         return fail(PA_ERR_INVALID_ARG, "workspace needs %zu bytes, 16-byte aligned (got %zu)",
@@ -382,6 +396,17 @@ pa_status pa::decode_impl(void* out, const void* q, pa_dtype q_dt, const void* k
     p.NB = NB;
     p.qk_scale = (float)((double)scale * (double)k_scale * 1.4426950408889634);
     p.v_scale = v_scale;
+    if (mod) {
+        if (mod->softcap > 0.f) {
+            p.qk_scale = (float)((double)scale * (double)k_scale / (double)mod->softcap);
+            p.cap_log2 = (float)((double)mod->softcap * 1.4426950408889634);
+            if (!std::isfinite(p.qk_scale) || !std::isfinite(p.cap_log2))
+                return fail(PA_ERR_INVALID_ARG, "scale / softcap or softcap is out of range");
+        }
+        p.slopes = mod->slopes;
+        p.window = mod->window;
+        p.key_start = mod->key_start;
+    }
     p.bs = bs;
     p.gc = gc;
     p.balanced = balanced || items ? 1 : 0;
@@ -418,10 +443,13 @@ pa_status pa::decode_impl(void* out, const void* q, pa_dtype q_dt, const void* k
 
     cudaError_t e;
     switch (cache_dt) {
-    case PA_F32: e = dec::launch_f32(L); break;
-    case PA_F16: e = dec::launch_f16(L); break;
-    case PA_BF16: e = dec::launch_bf16(L); break;
-    default: e = q_dt == PA_F16 ? dec::launch_fp8_q_f16(L) : dec::launch_fp8_q_bf16(L); break;
+    case PA_F32: e = mod ? dec::launch_scored_f32(L) : dec::launch_f32(L); break;
+    case PA_F16: e = mod ? dec::launch_scored_f16(L) : dec::launch_f16(L); break;
+    case PA_BF16: e = mod ? dec::launch_scored_bf16(L) : dec::launch_bf16(L); break;
+    default:
+        if (mod) e = q_dt == PA_F16 ? dec::launch_scored_fp8_q_f16(L) : dec::launch_scored_fp8_q_bf16(L);
+        else e = q_dt == PA_F16 ? dec::launch_fp8_q_f16(L) : dec::launch_fp8_q_bf16(L);
+        break;
     }
     if (e == cudaErrorNotSupported) return fail(PA_ERR_UNSUPPORTED, "no kernel for this shape");
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
@@ -443,4 +471,44 @@ extern "C" pa_status pa_decode(void* out, const void* q, pa_dtype q_dt, const vo
     return decode_impl(out, q, q_dt, key_cache, value_cache, cache_dt, block_tables, MB,
                        context_lens, S, Hq, Hkv, D, bs, NB, max_ctx, scale, k_scale, v_scale,
                        partition, workspace, workspace_bytes, stream, 0, 0, 0);
+}
+
+pa_status pa::check_score_opts(const ScoreOpts& o) {
+    if (!std::isfinite(o.softcap) || o.softcap < 0.f)
+        return fail(PA_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: none)");
+    if (o.window < 0) return fail(PA_ERR_INVALID_ARG, "window must be >= 0 (0: none)");
+    return PA_OK;
+}
+
+extern "C" pa_status pa_decode_scored_workspace_size(int S, int Hq, int D, int bs, int max_ctx,
+                                                     int window, int partition, size_t* bytes) {
+    clear_error();
+    if (bs <= 0 || window < 0 || max_ctx < 0 || partition < 0)
+        return fail(PA_ERR_INVALID_ARG, "negative or zero size");
+    return pa_decode_workspace_size(S, Hq, D, scored_span(max_ctx, window, bs), partition, bytes);
+}
+
+extern "C" pa_status pa_decode_scored(void* out, const void* q, pa_dtype q_dt,
+                                      const void* key_cache, const void* value_cache,
+                                      pa_dtype cache_dt, const int32_t* block_tables, int MB,
+                                      const int32_t* context_lens, int S, int Hq, int Hkv, int D,
+                                      int bs, int64_t NB, int max_ctx, float scale, float k_scale,
+                                      float v_scale, float softcap, const float* slopes,
+                                      int window, const int32_t* key_start, int partition,
+                                      void* workspace, size_t workspace_bytes,
+                                      pa_stream_t stream) {
+    PA_NVTX_RANGE("pa_decode_scored");
+    clear_error();
+    ScoreOpts o;
+    o.softcap = softcap;
+    o.slopes = slopes;
+    o.window = window;
+    o.key_start = key_start;
+    const pa_status st = check_score_opts(o);
+    if (st) return st;
+    if (partition < 0)
+        return fail(PA_ERR_INVALID_ARG, "partition must be >= 0 (no balanced grid)");
+    return decode_impl(out, q, q_dt, key_cache, value_cache, cache_dt, block_tables, MB,
+                       context_lens, S, Hq, Hkv, D, bs, NB, max_ctx, scale, k_scale, v_scale,
+                       partition, workspace, workspace_bytes, stream, 0, 0, 0, &o);
 }

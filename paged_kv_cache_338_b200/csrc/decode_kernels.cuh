@@ -84,6 +84,12 @@ struct Params {
                                  // ranges end at item boundaries), whose output it writes;
                                  // with fuse_prefix_blocks the regular items read their suffix
                                  // and fold the prefix_parts prefix records in
+    // modified scores (pa_decode_scored); the first visible key is also what
+    // the merge counts a sequence's partitions from
+    float cap_log2;              // softcap * log2(e), 0: none (qk_scale is then scale * k_scale / softcap)
+    const float* slopes;         // [Hq] distance bias slopes, or NULL
+    int window;                  // > 0: only the last `window` keys are visible
+    const int32_t* key_start;    // [S] first visible key, or NULL
     int rec_smem;                // one CTA per suffix: bytes of dynamic shared memory past the
                                  // barriers for its prefix records, fetched by a bulk copy while
                                  // the suffix streams (0: copied into the stages afterwards)
@@ -108,6 +114,13 @@ __device__ __forceinline__ int checked_len(const Params& p, int s, int bs) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// First visible key of sequence s of n tokens, in [0, n] (n: none is).
+__device__ __forceinline__ int first_visible(const Params& p, int s, int n) {
+    int lo = p.window > 0 ? n - p.window : 0;
+    if (p.key_start) lo = max(lo, p.key_start[s]);
+    return max(0, min(lo, n));
+}
+
 // BS is the tokens of one stage; PB the tokens of one physical cache block.
 // A stage holds PER = BS / PB consecutive blocks of a sequence (two blocks of
 // 8 tokens make a 16-token stage, so an 8-token cache pays the per-stage
@@ -121,11 +134,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 // and consumer warp w serves kv head w of the group over every stage: no warp
 // merge, no split of a head's blocks between warps.
 template <int DT_, int QT_, int BS_, int D_, int GC_, bool MMA_, int MROWS_ = 8, int PB_ = BS_,
-          int HG_ = 1>
+          int HG_ = 1, bool SCORED_ = false>
 struct Cfg {
     static constexpr int DT = DT_, QT = QT_, BS = BS_, D = D_, GC = GC_, MROWS = MROWS_;
     static constexpr int PB = PB_, PER = BS_ / PB_, HG = HG_;
     static constexpr bool MMA = MMA_;
+    static constexpr bool SCORED = SCORED_;  // scores are modified and masked (ScoreMod)
     static constexpr int E = dev::Storage<DT>::bytes;
     static constexpr int R = D * E;          // bytes of one token row of one kv head
     static constexpr int CH = R / 128;       // 128-byte segments per row
@@ -290,9 +304,41 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmk, const CUtensorMa
     *k_io = k;
 }
 
+// ------------------------------------------------------ modified scores
+// What a consumer needs to turn a product into a score (pa_decode_scored).  In
+// base-2 units, with x = qk_scale * <q, k> (qk_scale holds 1 / softcap when
+// there is a cap, else log2 e):
+//     z = cap_log2 * tanh(x)        (cap)      or  x
+//     z -= slope * (p - i)          (bias; slope in base-2 units, key i)
+// tanhf is the accurate one: the few scores a lane owns per stage hide behind
+// the stage's copy, so the decode stays bound by HBM.
+struct ScoreMod {
+    float cap_log2 = 0.f;
+    bool bias = false;
+    int first = 0;     // first visible token of the stage's rows (0: all of them)
+    int dist0 = 0;     // distance of the query to the stage's token 0
+};
+
+__device__ __forceinline__ float mod_score(const ScoreMod& x, float z, float slope, int t) {
+    if (x.cap_log2 > 0.f) z = x.cap_log2 * tanhf(z);
+    if (x.bias) z = fmaf(-slope, (float)(x.dist0 - t), z);
+    return z;
+}
+
+// The stage whose token 0 is token t0 of the sequence (n tokens, first visible lo).
+__device__ __forceinline__ ScoreMod stage_mod(const Params& p, int n, int lo, int t0) {
+    ScoreMod x;
+    x.cap_log2 = p.cap_log2;
+    x.bias = p.slopes != nullptr;
+    x.first = max(0, lo - t0);
+    x.dist0 = n - 1 - t0;
+    return x;
+}
+
 // --------------------------------------------------------- SIMT consumer
 template <class C>
 struct SimtState {
+    float slope[C::SCORED ? C::GC : 1];
     float q[C::GC][C::DPL];
     float acc[C::GC][C::DPL];
     float m[C::GC];
@@ -316,6 +362,7 @@ __device__ __forceinline__ void simt_load_q(SimtState<C>& st, const Params& p, i
         for (int j = 0; j < C::DPL; ++j) st.acc[g][j] = 0.f;
         st.m[g] = -INFINITY;
         st.l[g] = 0.f;
+        if constexpr (C::SCORED) st.slope[g] = p.slopes ? p.slopes[h0 + g] * kLog2e : 0.f;
     }
 }
 
@@ -342,7 +389,8 @@ __device__ __forceinline__ void simt_row(const uint8_t* tile, int t, int l8, flo
 
 template <class C>
 __device__ __forceinline__ void simt_block(SimtState<C>& st, const uint8_t* ktile,
-                                           const uint8_t* vtile, int nvalid) {
+                                           const uint8_t* vtile, int nvalid,
+                                           const ScoreMod& mod = {}) {
     const int lane = threadIdx.x & 31;
     const int l8 = lane & 7, grp = lane >> 3;
     constexpr int SUB = C::BS < 16 ? C::BS : 16;   // tokens per online-softmax update
@@ -363,7 +411,10 @@ __device__ __forceinline__ void simt_block(SimtState<C>& st, const uint8_t* ktil
                 a += __shfl_xor_sync(0xffffffffu, a, 1);
                 a += __shfl_xor_sync(0xffffffffu, a, 2);
                 a += __shfl_xor_sync(0xffffffffu, a, 4);
-                sc[it][g] = (t < nvalid) ? a : -INFINITY;
+                if constexpr (C::SCORED)
+                    sc[it][g] = t < nvalid && t >= mod.first ? mod_score(mod, a, st.slope[g], t)
+                                                             : -INFINITY;
+                else sc[it][g] = (t < nvalid) ? a : -INFINITY;
             }
         }
         #pragma unroll
@@ -384,7 +435,7 @@ __device__ __forceinline__ void simt_block(SimtState<C>& st, const uint8_t* ktil
         #pragma unroll
         for (int it = 0; it < IT; ++it) {
             const int t = sb * SUB + it * 4 + grp;
-            if (t < nvalid) {
+            if (t < nvalid && (!C::SCORED || t >= mod.first)) {
                 simt_row<C>(vtile, t, l8, f);
                 #pragma unroll
                 for (int g = 0; g < C::GC; ++g) {
@@ -530,6 +581,7 @@ struct MmaState {
     uint32_t qb[NH][KS][2];                  // B fragments of Q^T
     float o[NH][MD][4];                      // O^T accumulators
     float m[NH][2], l[NH][2];                // heads 2*tig, 2*tig+1 of each tile
+    float slope[C::SCORED ? NH : 1][2];
 };
 
 template <int QT>
@@ -590,6 +642,13 @@ __device__ __forceinline__ void mma_load_q(MmaState<C>& st, const Params& p, int
             for (int i = 0; i < 4; ++i) st.o[nh][md][i] = 0.f;
         st.m[nh][0] = st.m[nh][1] = -INFINITY;
         st.l[nh][0] = st.l[nh][1] = 0.f;
+        if constexpr (C::SCORED) {
+            #pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int hd = nh * 8 + 2 * tig + j;
+                st.slope[nh][j] = p.slopes && hd < G ? p.slopes[h0 + hd] * kLog2e : 0.f;
+            }
+        }
     }
 }
 
@@ -601,7 +660,7 @@ __device__ __forceinline__ uint32_t chunk_addr(uint32_t tile, int t, int c) {
 
 template <class C>
 __device__ __forceinline__ void mma_block(MmaState<C>& st, uint8_t* ktile_p, uint8_t* vtile_p,
-                                          int nvalid, float qk_scale) {
+                                          int nvalid, float qk_scale, const ScoreMod& mod = {}) {
     using S = MmaState<C>;
     constexpr int BS = C::BS;
     constexpr int CT = S::CT;
@@ -703,11 +762,21 @@ __device__ __forceinline__ void mma_block(MmaState<C>& st, uint8_t* ktile_p, uin
         #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int t0 = mt * 16 + gid, t1 = t0 + 8;
-            const bool v0 = t0 < nvalid, v1 = (BS >= 16) && t1 < nvalid;
+            const bool v0 = t0 < nvalid && (!C::SCORED || t0 >= mod.first);
+            const bool v1 = (BS >= 16) && t1 < nvalid && (!C::SCORED || t1 >= mod.first);
+            if constexpr (C::SCORED) {
+                #pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sc[mt][nh][i] = (i < 2 ? v0 : v1)
+                                        ? mod_score(mod, sc[mt][nh][i] * qk_scale,
+                                                    st.slope[nh][i & 1], i < 2 ? t0 : t1)
+                                        : -INFINITY;
+            } else {
             sc[mt][nh][0] = v0 ? sc[mt][nh][0] * qk_scale : -INFINITY;
             sc[mt][nh][1] = v0 ? sc[mt][nh][1] * qk_scale : -INFINITY;
             sc[mt][nh][2] = v1 ? sc[mt][nh][2] * qk_scale : -INFINITY;
             sc[mt][nh][3] = v1 ? sc[mt][nh][3] * qk_scale : -INFINITY;
+            }
             bm0 = fmaxf(bm0, fmaxf(sc[mt][nh][0], sc[mt][nh][2]));
             bm1 = fmaxf(bm1, fmaxf(sc[mt][nh][1], sc[mt][nh][3]));
         }
@@ -756,7 +825,10 @@ __device__ __forceinline__ void mma_block(MmaState<C>& st, uint8_t* ktile_p, uin
     if constexpr (S::FP8) {
         const uint32_t vt = dev::smem_addr(vtile_p);
         const int tig = lane & 3;
-        const bool tail = nvalid < BS;
+        // scored: the codes of tokens before the first visible one too
+        const int first = C::SCORED ? mod.first : 0;
+        const bool tail = nvalid < BS || first > 0;
+        auto seen = [&](int t) { return t < nvalid && (!C::SCORED || t >= first); };
         if constexpr (BS >= 16) {
             // one pass over the tile; TAIL: codes of tokens at or past nvalid are
             // zeroed first (a zero weight times a NaN code would still be NaN)
@@ -768,8 +840,8 @@ __device__ __forceinline__ void mma_block(MmaState<C>& st, uint8_t* ktile_p, uin
                     uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
                     if constexpr (TAIL) {
                         const int t0 = kt * 16 + 2 * tig;
-                        keep0 = (t0 < nvalid ? 0x0000ffffu : 0u) | (t0 + 1 < nvalid ? 0xffff0000u : 0u);
-                        keep1 = (t0 + 8 < nvalid ? 0x0000ffffu : 0u) | (t0 + 9 < nvalid ? 0xffff0000u : 0u);
+                        keep0 = (seen(t0) ? 0x0000ffffu : 0u) | (seen(t0 + 1) ? 0xffff0000u : 0u);
+                        keep1 = (seen(t0 + 8) ? 0x0000ffffu : 0u) | (seen(t0 + 9) ? 0xffff0000u : 0u);
                     }
                     #pragma unroll
                     for (int md = 0; md < S::MD; md += 2) {
@@ -803,7 +875,7 @@ __device__ __forceinline__ void mma_block(MmaState<C>& st, uint8_t* ktile_p, uin
         } else {
             uint32_t keep = 0xffffffffu;
             if (tail)
-                keep = (2 * tig < nvalid ? 0x0000ffffu : 0u) | (2 * tig + 1 < nvalid ? 0xffff0000u : 0u);
+                keep = (seen(2 * tig) ? 0x0000ffffu : 0u) | (seen(2 * tig + 1) ? 0xffff0000u : 0u);
             #pragma unroll
             for (int md = 0; md < S::MD; md += 4) {
                 // matrices: tokens 0-7 of chunks md, md+1, md+2, md+3
@@ -828,6 +900,17 @@ __device__ __forceinline__ void mma_block(MmaState<C>& st, uint8_t* ktile_p, uin
                                           (i % 8) * 16) = make_uint4(0, 0, 0, 0);
             }
             __syncwarp();
+        }
+        if constexpr (C::SCORED) {
+            // the rows before the first visible token likewise
+            if (mod.first > 0) {
+                for (int i = lane; i < mod.first * C::CH * 8; i += 32) {
+                    const int t = i / (C::CH * 8), k = (i / 8) % C::CH;
+                    *reinterpret_cast<uint4*>(vtile_p + k * C::SEGSTRIDE + tile_row<C>(t) * 128 +
+                                              (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                __syncwarp();
+            }
         }
         const uint32_t vtile = dev::smem_addr(vtile_p);
         if constexpr (BS >= 16) {
@@ -860,7 +943,8 @@ __device__ __forceinline__ void mma_block(MmaState<C>& st, uint8_t* ktile_p, uin
         }
     }
     if constexpr (!S::FP8) {
-        if (nvalid < BS) dev::fence_proxy_async_smem();   // generic writes before the next TMA fill
+        if (nvalid < BS || (C::SCORED && mod.first > 0))
+            dev::fence_proxy_async_smem();   // generic writes before the next TMA fill
     }
 }
 
@@ -1064,7 +1148,16 @@ decode_partition(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
     const int pre = (threadIdx.x >> 5) == C::NW ? table_entry_ahead(p, s, pblk0_guess) : 0;
     const int n = checked_len(p, s, C::PB);
     const int nphys_all = (n + C::PB - 1) / C::PB;
-    const int nblk_all = (n + C::BS - 1) / C::BS;
+    int nblk_all = (n + C::BS - 1) / C::BS;
+    // scored: stages before the first visible key are not read (their table
+    // entries may name no block any more), and partitions count from its stage
+    int lo = 0, stage0 = 0;
+    if constexpr (C::SCORED) {
+        lo = first_visible(p, s, n);
+        stage0 = min(lo / C::BS, nblk_all);
+        if (lo >= n) stage0 = nblk_all;         // nothing is visible: an empty sequence
+        nblk_all -= stage0;
+    }
     int blk0 = 0, nblk = nblk_all, nparts = 1;
     int q0 = part, nq = 1;                      // partitions (records) this CTA writes
     bool fuse_records = false;
@@ -1123,6 +1216,7 @@ decode_partition(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         nparts = max(1, (nblk_all + p.part_blocks - 1) / p.part_blocks);
         nq = min(p.part_group, nparts - q0);
     }
+    if constexpr (C::SCORED) blk0 += stage0;
     if (part > 0 && nblk <= 0) return;          // this sequence has fewer partitions
     nblk = max(nblk, 0);
 
@@ -1184,7 +1278,8 @@ decode_partition(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     }
                     uint8_t* kt = stages + (size_t)stg * C::STAGE + hw * C::PB * 128;
                     const int nvalid = min(C::BS, n - (blk0 + j) * C::BS);
-                    mma_block<C>(st, kt, kt + C::TILE, nvalid, p.qk_scale);
+                    mma_block<C>(st, kt, kt + C::TILE, nvalid, p.qk_scale,
+                                     stage_mod(p, n, lo, (blk0 + j) * C::BS));
                     __syncwarp();
                     if (lane == 0) dev::mbar_arrive(empty0 + 8 * stg);
                     if (*(volatile int*)&s_abort) { stop = true; break; }
@@ -1228,8 +1323,9 @@ decode_partition(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     uint8_t* kt = stages + (size_t)stg * C::STAGE;
                     const int nvalid = min(C::BS, n - (blk0 + j) * C::BS);
                     if constexpr (C::MMA)
-                        mma_block<C>(st, kt, kt + C::TILE, nvalid, p.qk_scale);
-                    else simt_block<C>(st, kt, kt + C::TILE, nvalid);
+                        mma_block<C>(st, kt, kt + C::TILE, nvalid, p.qk_scale,
+                                     stage_mod(p, n, lo, (blk0 + j) * C::BS));
+                    else simt_block<C>(st, kt, kt + C::TILE, nvalid, stage_mod(p, n, lo, (blk0 + j) * C::BS));
                     __syncwarp();
                     if (lane == 0) dev::mbar_arrive(empty0 + 8 * stg);
                     if (*(volatile int*)&s_abort) stop = true;
@@ -1320,8 +1416,9 @@ decode_partition(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             uint8_t* kt = stages + (size_t)stg * C::STAGE + hw * C::PB * 128;
             const int nvalid = min(C::BS, n - (blk0 + j) * C::BS);
             if constexpr (C::MMA)
-                mma_block<C>(st, kt, kt + C::TILE, nvalid, p.qk_scale);
-            else simt_block<C>(st, kt, kt + C::TILE, nvalid);
+                mma_block<C>(st, kt, kt + C::TILE, nvalid, p.qk_scale,
+                                     stage_mod(p, n, lo, (blk0 + j) * C::BS));
+            else simt_block<C>(st, kt, kt + C::TILE, nvalid, stage_mod(p, n, lo, (blk0 + j) * C::BS));
             __syncwarp();
             if (lane == 0) dev::mbar_arrive(empty0 + 8 * stg);
             if (*(volatile int*)&s_abort) break;
@@ -1904,7 +2001,12 @@ __global__ void __launch_bounds__(NWARPS * 32) decode_merge(const Params p, int 
         row0 = sane ? (size_t)(item + fl.x) * gc + (head_ok ? h : 0) % gc : 0;
         stride = (size_t)gc;
     } else {
-        count = min(p.max_parts, (n + p.part_tokens - 1) / p.part_tokens);
+        int tokens = n;
+        if (p.window > 0 || p.key_start) {      // partitions count from the first visible stage
+            const int stage = p.part_tokens / p.part_blocks, lo = first_visible(p, s, n);
+            tokens = lo < n ? n - lo / stage * stage : 0;
+        }
+        count = min(p.max_parts, (tokens + p.part_tokens - 1) / p.part_tokens);
         if (count <= 1 && !p.force_ws) return;        // CTA-uniform: written by the partition kernel
         row0 = ((size_t)s * p.Hq + (head_ok ? h : 0)) * p.max_parts;
         stride = 1;

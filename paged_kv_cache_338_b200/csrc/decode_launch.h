@@ -34,11 +34,18 @@ cudaError_t launch_f16(const Launch& L);
 cudaError_t launch_bf16(const Launch& L);
 cudaError_t launch_fp8_q_f16(const Launch& L);
 cudaError_t launch_fp8_q_bf16(const Launch& L);
+// the same with modified scores (pa_decode_scored)
+cudaError_t launch_scored_f32(const Launch& L);
+cudaError_t launch_scored_f16(const Launch& L);
+cudaError_t launch_scored_bf16(const Launch& L);
+cudaError_t launch_scored_fp8_q_f16(const Launch& L);
+cudaError_t launch_scored_fp8_q_bf16(const Launch& L);
 
 template <class C>
 cudaError_t launch_one(const Launch& L) {
-    if constexpr (C::PER != 1 || C::HG != 1) {
-        // the host pairs blocks and groups heads for the partition kernel only
+    if constexpr (C::PER != 1 || C::HG != 1 || C::SCORED) {
+        // the host pairs blocks, groups heads and modifies scores for the
+        // partition kernel only
         if (L.balanced) return cudaErrorNotSupported;
     } else if (L.balanced) {
         auto kern = decode_balanced<C>;
@@ -98,7 +105,7 @@ constexpr bool row_ok() {
 }
 
 // BS: tokens per stage; PB: tokens per physical block (BS / PB blocks a stage)
-template <int DT, int QT, int BS, int D, int PB>
+template <int DT, int QT, int BS, int D, int PB, bool SC>
 cudaError_t launch_by_heads(const Launch& L) {
     if constexpr (!row_ok<DT, D>()) {
         return cudaErrorNotSupported;
@@ -107,42 +114,43 @@ cudaError_t launch_by_heads(const Launch& L) {
             if constexpr (((DT == QT && (DT == PA_F16 || DT == PA_BF16)) || DT == PA_FP8_E4M3) &&
                           D <= 128) {
                 if (L.hg == 4) {
-                    if (L.mrows == 8) return launch_one<Cfg<DT, QT, BS, D, 8, true, 8, PB, 4>>(L);
-                    return launch_one<Cfg<DT, QT, BS, D, 16, true, 16, PB, 4>>(L);
+                    if (L.mrows == 8) return launch_one<Cfg<DT, QT, BS, D, 8, true, 8, PB, 4, SC>>(L);
+                    return launch_one<Cfg<DT, QT, BS, D, 16, true, 16, PB, 4, SC>>(L);
                 }
-                if (L.mrows == 8) return launch_one<Cfg<DT, QT, BS, D, 8, true, 8, PB>>(L);
-                return launch_one<Cfg<DT, QT, BS, D, 16, true, 16, PB>>(L);
+                if (L.mrows == 8) return launch_one<Cfg<DT, QT, BS, D, 8, true, 8, PB, 1, SC>>(L);
+                return launch_one<Cfg<DT, QT, BS, D, 16, true, 16, PB, 1, SC>>(L);
             } else {
                 return cudaErrorNotSupported;
             }
         }
         switch (L.gc) {
-        case 1: return launch_one<Cfg<DT, QT, BS, D, 1, false, 8, PB>>(L);
-        case 2: return launch_one<Cfg<DT, QT, BS, D, 2, false, 8, PB>>(L);
+        case 1: return launch_one<Cfg<DT, QT, BS, D, 1, false, 8, PB, 1, SC>>(L);
+        case 2: return launch_one<Cfg<DT, QT, BS, D, 2, false, 8, PB, 1, SC>>(L);
         case 4:
-            if constexpr (D <= 128) return launch_one<Cfg<DT, QT, BS, D, 4, false, 8, PB>>(L);
+            if constexpr (D <= 128) return launch_one<Cfg<DT, QT, BS, D, 4, false, 8, PB, 1, SC>>(L);
             else return cudaErrorNotSupported;
         }
         return cudaErrorNotSupported;
     }
 }
 
-template <int DT, int QT, int BS, int PB>
+template <int DT, int QT, int BS, int PB, bool SC>
 cudaError_t launch_by_dim(const Launch& L) {
     switch (L.D) {
-    case 64: return launch_by_heads<DT, QT, BS, 64, PB>(L);
-    case 128: return launch_by_heads<DT, QT, BS, 128, PB>(L);
-    case 256: return launch_by_heads<DT, QT, BS, 256, PB>(L);
+    case 64: return launch_by_heads<DT, QT, BS, 64, PB, SC>(L);
+    case 128: return launch_by_heads<DT, QT, BS, 128, PB, SC>(L);
+    case 256: return launch_by_heads<DT, QT, BS, 256, PB, SC>(L);
     }
     return cudaErrorNotSupported;
 }
 
-template <int DT, int QT>
+template <int DT, int QT, bool SC = false>
 cudaError_t launch_dtype(const Launch& L) {
     switch (L.bs) {
-    case 8: return L.pair ? launch_by_dim<DT, QT, 16, 8>(L) : launch_by_dim<DT, QT, 8, 8>(L);
-    case 16: return launch_by_dim<DT, QT, 16, 16>(L);
-    case 32: return launch_by_dim<DT, QT, 32, 32>(L);
+    case 8:
+        return L.pair ? launch_by_dim<DT, QT, 16, 8, SC>(L) : launch_by_dim<DT, QT, 8, 8, SC>(L);
+    case 16: return launch_by_dim<DT, QT, 16, 16, SC>(L);
+    case 32: return launch_by_dim<DT, QT, 32, 32, SC>(L);
     }
     return cudaErrorNotSupported;
 }

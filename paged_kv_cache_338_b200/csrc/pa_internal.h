@@ -72,18 +72,31 @@ void* symbol_address(const void* symbol, SymbolCache* cache, const char* what);
 // Translate a CUDA runtime error into PA_ERR_CUDA with context.
 pa_status cuda_fail(int err, const char* what);
 
+// Score modifications and masks of pa_decode_scored / pa_prefill_scored.
+struct ScoreOpts {
+    float softcap = 0.f;                 // > 0: z = softcap * tanh(z / softcap)
+    const float* slopes = nullptr;       // device [Hq]: z -= slope * |key - query position|
+    int window = 0;                      // > 0: keys at distance >= window are not visible
+    const int32_t* key_start = nullptr;  // device: first visible key per sequence / new token
+};
+
+// The checks both entry points share.
+pa_status check_score_opts(const ScoreOpts& o);
+
 // pa_decode with the shared-prefix switches (decode_host.cu): partitions
 // below prefix_parts of sequences whose table starts with row 0's blocks are
 // left to the caller's prefix records; force_ws sends every record through
 // the workspace and always runs the merge.  With fuse_prefix_blocks > 0 one
 // CTA per (sequence, kv head) reads the suffix past that many blocks and
-// merges the prefix_parts records itself (no merge kernel).
+// merges the prefix_parts records itself (no merge kernel).  `mod` non-NULL:
+// modified scores (plain single-pass and split-K decode only).
 pa_status decode_impl(void* out, const void* q, pa_dtype q_dt, const void* key_cache,
                       const void* value_cache, pa_dtype cache_dt, const int32_t* block_tables,
                       int MB, const int32_t* context_lens, int S, int Hq, int Hkv, int D, int bs,
                       int64_t NB, int max_ctx, float scale, float k_scale, float v_scale,
                       int partition, void* workspace, size_t workspace_bytes, pa_stream_t stream,
-                      int prefix_parts, int force_ws, int fuse_prefix_blocks);
+                      int prefix_parts, int force_ws, int fuse_prefix_blocks,
+                      const ScoreOpts* mod = nullptr);
 
 // Shared-prefix decode, step 1 (prefill.cu): split-K records (m, l, o * v_scale)
 // of partitions 0 .. prefix_tokens / chunk_tokens - 1 of every (sequence, head),
