@@ -443,6 +443,59 @@ pa_status pa_prefill(void* out, const void* q, pa_dtype q_dt, const void* key_ca
                      int T, int Hq, int Hkv, int D, int bs, int64_t NB, int max_query_len,
                      float scale, pa_stream_t stream);
 
+/*
+ * pa_prefill with modified scores and masks, over caches of the queries' dtype
+ * or fp8, also for a few new tokens on long contexts.  (The pages have no
+ * counterpart.)  New token t of sequence s, the l-th of L new ones, sits at
+ * position p = n - L + l (n = context_lens[s]); for key i of its sequence
+ *
+ *   z_i = scale * <q[t, h, :], k_i>
+ *   z_i = softcap * tanh(z_i / softcap)          softcap > 0 (0: none)
+ *   z_i = z_i - slopes[h] * |i - p|              slopes not NULL, fp32 [Hq]
+ *   out[t, h, :] = sum_i softmax(z)_i v_i over the visible keys, those with
+ *       i <= p, or i < prefix_lens[s]            prefix_lens not NULL, int32 [S]:
+ *                                                leading keys every new token sees
+ *                                                (cut to n)
+ *       p - i < window                           window > 0 (0: no window)
+ *       i >= key_start[t]                        key_start not NULL, int32 [T]:
+ *                                                the token's own document starts there
+ *
+ * A token with no visible key gives a zero row.  Keys and values a token does
+ * not see do not reach its rows, whatever they hold (infinities and NaN too).
+ * Blocks past the last key that some token of a sequence sees, and those before
+ * the first, are not read, and their table entries may be anything.  A visible
+ * block outside [0, NB) reads as zeros and sets PA_DEV_BAD_BLOCK.
+ *
+ *   out, q       [T, Hq, D] f16 or bf16; cache_dt the same, or PA_FP8_E4M3 with
+ *                k_scale, v_scale (else both 1).  D 64 or 128 (fp8: 128); bs 8, 16
+ *                or 32; Hq / Hkv 1, 2, 4, 8 or 16.  scale > 0.
+ *   query_start  int32 [S + 1], not decreasing; rows of out outside every
+ *                [query_start[s], query_start[s + 1]) are left as they are.  A
+ *                sequence with more new tokens than max_query_len or n, with
+ *                n > max_ctx or MB * bs, or with rows outside [0, T) is skipped and
+ *                sets PA_DEV_BAD_CONTEXT.
+ *   partition    0, or a multiple of 128: the keys of every pair of query tiles
+ *                are split over CTAs in parts of this many, joined by a second
+ *                kernel; pa_prefill_scored_suggest_partition() gives a value for
+ *                the largest sizes of a batch.
+ *   workspace    pa_prefill_scored_workspace_size() bytes, 16-byte aligned (0 bytes
+ *                needed: may be NULL); calls that overlap need one each.
+ * Results with the same arguments are the same bit for bit.
+ */
+pa_status pa_prefill_scored_suggest_partition(int S, int Hq, int Hkv, int max_query_len,
+                                              int max_ctx, int window, int* partition);
+pa_status pa_prefill_scored_workspace_size(int S, int T, int Hq, int D, int max_query_len,
+                                           int max_ctx, int window, int partition, size_t* bytes);
+pa_status pa_prefill_scored(void* out, const void* q, pa_dtype q_dt, const void* key_cache,
+                            const void* value_cache, pa_dtype cache_dt,
+                            const int32_t* block_tables, int MB, const int32_t* context_lens,
+                            const int32_t* query_start, int S, int T, int Hq, int Hkv, int D,
+                            int bs, int64_t NB, int max_query_len, int max_ctx, float scale,
+                            float k_scale, float v_scale, float softcap, const float* slopes,
+                            int window, const int32_t* key_start, const int32_t* prefix_lens,
+                            int partition, void* workspace, size_t workspace_bytes,
+                            pa_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * Host block pool -- "PagedAttention 机制" §5.3.4 (BlockAllocator: free list,
  * per-block reference count, allocate / free / incr_ref, out-of-memory when

@@ -22,7 +22,8 @@ __all__ = [
     "PaError", "lib", "pa_version", "pa_launch_count", "pa_last_error", "pa_device_status",
     "pa_reshape_and_cache", "pa_norm_rope_append", "pa_copy_blocks", "pa_decode", "pa_decode_workspace_size",
     "pa_decode_suggest_partition", "pa_decode_partition_group", "pa_decode_select", "pa_decode_noalloc", "pa_prefill",
-    "pa_decode_scored", "pa_decode_scored_workspace_size",
+    "pa_decode_scored", "pa_decode_scored_workspace_size", "pa_prefill_scored",
+    "pa_prefill_scored_suggest_partition", "pa_prefill_scored_workspace_size",
     "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_size",
     "BlockPool", "pa_plan_shards",
     "PA_DEV_BAD_SLOT", "PA_DEV_BAD_BLOCK", "PA_DEV_WAIT_TIMEOUT", "PA_DEV_BAD_CONTEXT",
@@ -90,6 +91,10 @@ def lib() -> ctypes.CDLL:
                               P, I, P, SZ, P], I),
         "pa_decode_noalloc": ([P, P, I, P, P, I, P, I, P, I, I, I, I, I, I64, I, F, F, F, I, P], I),
         "pa_prefill": ([P, P, I, P, P, I, P, I, P, P, I, I, I, I, I, I, I64, I, F, P], I),
+        "pa_prefill_scored_suggest_partition": ([I, I, I, I, I, I, ctypes.POINTER(I)], I),
+        "pa_prefill_scored_workspace_size": ([I, I, I, I, I, I, I, I, ctypes.POINTER(SZ)], I),
+        "pa_prefill_scored": ([P, P, I, P, P, I, P, I, P, P, I, I, I, I, I, I, I64, I, I, F, F, F,
+                               F, P, I, P, P, I, P, SZ, P], I),
         "pa_decode_shared_prefix_workspace_size": ([I, I, I, I, I, I, I, I, ctypes.POINTER(SZ)], I),
         "pa_decode_shared_prefix": ([P, P, I, P, P, I, P, I, P, I, I, I, I, I, I64, I, F, F, F, I,
                                      P, SZ, P], I),
@@ -462,6 +467,58 @@ def pa_prefill(out: torch.Tensor, q: torch.Tensor, key_cache: torch.Tensor,
                             _dt(key_cache), _ptr(block_tables), MB, _ptr(context_lens),
                             _ptr(query_start), S, T, Hq, Hkv, D, bs, NB, int(max_query_len),
                             float(scale), _stream(stream)))
+
+
+def pa_prefill_scored_suggest_partition(S: int, Hq: int, Hkv: int, max_query_len: int,
+                                        max_ctx: int, window: int) -> int:
+    """Keys per part for a batch of these largest sizes (0: no split)."""
+    n = ctypes.c_int(0)
+    _check(lib().pa_prefill_scored_suggest_partition(S, Hq, Hkv, max_query_len, max_ctx, window,
+                                                     ctypes.byref(n)))
+    return n.value
+
+
+def pa_prefill_scored_workspace_size(S: int, T: int, Hq: int, D: int, max_query_len: int,
+                                     max_ctx: int, window: int, partition: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().pa_prefill_scored_workspace_size(S, T, Hq, D, max_query_len, max_ctx, window,
+                                                  partition, ctypes.byref(n)))
+    return n.value
+
+
+def pa_prefill_scored(out: torch.Tensor, q: torch.Tensor, key_cache: torch.Tensor,
+                      value_cache: torch.Tensor, block_tables: torch.Tensor,
+                      context_lens: torch.Tensor, query_start: torch.Tensor, max_query_len: int,
+                      max_ctx: int, scale: float, softcap: float = 0.0,
+                      slopes: Optional[torch.Tensor] = None, window: int = 0,
+                      key_start: Optional[torch.Tensor] = None,
+                      prefix_lens: Optional[torch.Tensor] = None, k_scale: float = 1.0,
+                      v_scale: float = 1.0, partition: int = 0,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """pa_prefill with modified scores: softcap (tanh cap, 0: none), slopes (fp32
+    [Hq], distance bias), window (last keys visible, 0: all), key_start (int32
+    [T], first visible key per new token), prefix_lens (int32 [S], leading keys
+    every new token sees).  The cache may be fp8 (k_scale, v_scale).
+    workspace: pa_prefill_scored_workspace_size()."""
+    _attention_args(out, q, key_cache, value_cache, block_tables, context_lens, slopes)
+    T, Hq, D = q.shape
+    NB, bs, Hkv, _ = key_cache.shape
+    S = context_lens.numel()
+    if query_start.dtype != torch.int32 or query_start.numel() != S + 1:
+        raise PaError(1, "query_start must hold S + 1 int32 offsets")
+    if key_start is not None and (key_start.dtype != torch.int32 or key_start.numel() != T):
+        raise PaError(1, "key_start must hold T int32 positions")
+    if prefix_lens is not None and (prefix_lens.dtype != torch.int32 or prefix_lens.numel() != S):
+        raise PaError(1, "prefix_lens must hold S int32 lengths")
+    _on_current_device(out, q, key_cache, value_cache, block_tables, context_lens, query_start,
+                       slopes, key_start, prefix_lens, workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().pa_prefill_scored(
+        _ptr(out), _ptr(q), _dt(q), _ptr(key_cache), _ptr(value_cache), _dt(key_cache),
+        _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), _ptr(query_start), S, T, Hq,
+        Hkv, D, bs, NB, max_query_len, max_ctx, scale, k_scale, v_scale, softcap, _ptr(slopes),
+        window, _ptr(key_start), _ptr(prefix_lens), partition, _ptr(workspace), ws_bytes,
+        _stream(stream)))
 
 
 def pa_plan_shards(context_lens, ndev: int):

@@ -397,12 +397,8 @@ pa_status pa::decode_impl(void* out, const void* q, pa_dtype q_dt, const void* k
     p.qk_scale = (float)((double)scale * (double)k_scale * 1.4426950408889634);
     p.v_scale = v_scale;
     if (mod) {
-        if (mod->softcap > 0.f) {
-            p.qk_scale = (float)((double)scale * (double)k_scale / (double)mod->softcap);
-            p.cap_log2 = (float)((double)mod->softcap * 1.4426950408889634);
-            if (!std::isfinite(p.qk_scale) || !std::isfinite(p.cap_log2))
-                return fail(PA_ERR_INVALID_ARG, "scale / softcap or softcap is out of range");
-        }
+        chk = check_score_opts(*mod, scale, k_scale, 1.0, &p.qk_scale, &p.cap_log2);
+        if (chk) return chk;
         p.slopes = mod->slopes;
         p.window = mod->window;
         p.key_start = mod->key_start;
@@ -473,10 +469,17 @@ extern "C" pa_status pa_decode(void* out, const void* q, pa_dtype q_dt, const vo
                        partition, workspace, workspace_bytes, stream, 0, 0, 0);
 }
 
-pa_status pa::check_score_opts(const ScoreOpts& o) {
+pa_status pa::check_score_opts(const ScoreOpts& o, double scale, double k_scale, double cap_factor,
+                               float* qk, float* cap_log2) {
     if (!std::isfinite(o.softcap) || o.softcap < 0.f)
         return fail(PA_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: none)");
     if (o.window < 0) return fail(PA_ERR_INVALID_ARG, "window must be >= 0 (0: none)");
+    const double log2e = 1.4426950408889634;
+    const bool cap = o.softcap > 0.f;
+    *qk = (float)(scale * k_scale * (cap ? cap_factor / (double)o.softcap : log2e));
+    *cap_log2 = cap ? (float)((double)o.softcap * log2e) : 0.f;
+    if (!std::isfinite(*qk) || !std::isfinite(*cap_log2) || (cap && !(*cap_log2 > 0.f)))
+        return fail(PA_ERR_INVALID_ARG, "scale, softcap or scale / softcap is out of range");
     return PA_OK;
 }
 
@@ -504,7 +507,8 @@ extern "C" pa_status pa_decode_scored(void* out, const void* q, pa_dtype q_dt,
     o.slopes = slopes;
     o.window = window;
     o.key_start = key_start;
-    const pa_status st = check_score_opts(o);
+    float qk, cap;
+    const pa_status st = check_score_opts(o, scale, k_scale, 1.0, &qk, &cap);
     if (st) return st;
     if (partition < 0)
         return fail(PA_ERR_INVALID_ARG, "partition must be >= 0 (no balanced grid)");

@@ -80,8 +80,11 @@ struct ScoreOpts {
     const int32_t* key_start = nullptr;  // device: first visible key per sequence / new token
 };
 
-// The checks both entry points share.
-pa_status check_score_opts(const ScoreOpts& o);
+// The checks both entry points share, and the factors the kernels take: with a
+// cap *qk = cap_factor * scale * k_scale / softcap and *cap_log2 = softcap * log2 e,
+// else scale * k_scale * log2 e and 0.
+pa_status check_score_opts(const ScoreOpts& o, double scale, double k_scale, double cap_factor,
+                           float* qk, float* cap_log2);
 
 // pa_decode with the shared-prefix switches (decode_host.cu): partitions
 // below prefix_parts of sequences whose table starts with row 0's blocks are

@@ -1,0 +1,46 @@
+// Between the host entry of pa_prefill_scored and its kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace ps {
+
+constexpr int kPairGroup = 16;    // adjacent tile pairs scheduled side by side
+
+struct Params {
+    void* out;
+    const void* v_cache;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* query_start;
+    const int32_t* key_start;     // [T] first visible key per new token, or NULL
+    const int32_t* prefix_lens;   // [S] leading keys every new token sees, or NULL
+    const float* slopes;          // [Hq], or NULL
+    unsigned int* err;
+    long long NB;
+    int T, Hq, G, log2G, TQ, MB, bs, log2bs, max_qlen, max_ctx, n_pairs, pair_group;
+    int window;                   // > 0: keys at distance >= window are not visible
+    int part_tiles, max_parts;    // key tiles per part; parts of a row at most
+    float sl;                     // scale * k_scale * log2 e, with a cap 2 * scale * k_scale / softcap
+    float cap_log2;               // softcap * log2 e, 0: none
+    float v_scale;
+    float2* ws_ml;                // [T, Hq, max_parts] (m, l)
+    float* ws_o;                  // [T, Hq, max_parts, D]
+};
+
+struct Launch {
+    const CUtensorMap *mq, *mk, *mv;
+    const Params* p;
+    dim3 grid;
+    cudaStream_t stream;
+};
+
+cudaError_t launch_bf16(const Launch& a, int D);
+cudaError_t launch_f16(const Launch& a, int D);
+cudaError_t launch_fp8_q_bf16(const Launch& a, int D);
+cudaError_t launch_fp8_q_f16(const Launch& a, int D);
+
+}  // namespace ps

@@ -1,0 +1,6 @@
+// Instantiations of the modified-score chunk attention: f16 queries and cache.
+#include "prefill_scored.cuh"
+
+cudaError_t ps::launch_f16(const Launch& a, int D) {
+    return D == 64 ? launch_mod<PA_F16, false, 64>(a) : launch_mod<PA_F16, false, 128>(a);
+}

@@ -96,8 +96,6 @@ def check(c, got, what, want=None):
     assert torch.equal(torch.isnan(g), nan), \
         f"{what}: NaN pattern differs at {torch.nonzero(torch.isnan(g) != nan)[:4].tolist()}"
     p_dt = {"f32": None, "fp8": torch.float16}.get(c["cdt"], DT[c["dt"]])
-    if c["cdt"] == "fp8" and not c["decode"]:
-        p_dt = DT[c["dt"]]
     fine = torch.isfinite(b.out)
     assert torch.equal(g[~fine & ~nan], b.out[~fine & ~nan]), f"{what}: infinities"
     tol = b.tolerance(DT[c["dt"]], p_dt, c["q"].shape[2])
