@@ -101,9 +101,9 @@ extern "C" pa_status pa_prefill_scored(
     o.slopes = slopes;
     o.window = window;
     o.key_start = key_start;
-    // with a cap the kernel works on u = 2 z / softcap
+    // with a cap the kernel works on u = 4 z / softcap
     float sl, cap_log2;
-    pa_status st = pa::check_score_opts(o, scale, k_scale, 2.0, &sl, &cap_log2);
+    pa_status st = pa::check_score_opts(o, scale, k_scale, 4.0, &sl, &cap_log2);
     if (!st) st = check_sizes(max_query_len, max_ctx, window, partition);
     if (st) return st;
     if (!std::isfinite(scale) || !(scale > 0.f))

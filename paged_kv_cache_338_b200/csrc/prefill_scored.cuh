@@ -37,11 +37,13 @@
 // product.  In tiles that some row masks, a warp looks through V (one multiply
 // by zero per two elements) and sets non-finite elements to zero before the
 // product; the epilogue then adds them back to the rows that do see their key,
-// reading them from the cache.  Tiles that all rows see whole need neither.
+// reading them from the cache.  Tiles that all rows see whole need neither.  The
+// MMA warps do the look while they wait for P anyway (880 of its 2600 cycles).
 //
 // Warps: 0-3 and 4-7 softmax and epilogue of halves A and B; 8 copies; 9 and 10
-// the MMAs of A and B; 11 the look through V; 8-bit: 12-15 widening.  Tensor
-// memory: S_A 0..127, O_A 128..255, S_B 256..383, O_B 384..511.  Every wait is
+// the MMAs of A and B, and the look through V; 11 completes their warpgroup; 8-bit:
+// 12-15 widening.  The softmax warps w and w + 4 share a scheduler and take turns
+// with their exponentials (A, B, A, ...), as in pa_prefill.  Tensor memory: S_A 0..127, O_A 128..255, S_B 256..383, O_B 384..511.  Every wait is
 // bounded (2 s): then PA_DEV_WAIT_TIMEOUT is set and the CTA drains its copies
 // and MMAs, frees its tensor memory and exits.
 #pragma once
@@ -69,7 +71,7 @@ template <bool FP8, int D>
 struct Plan {
     static constexpr int NSEG = D / 64;              // 128-byte segments of an operand row
     static constexpr int TILE = NSEG * kSeg;         // 128 rows of D operand elements
-    // operand slots, K_j and V_j in turn (16-bit: V in the odd ones)
+    // operand slots, K_j and V_j in turn
     static constexpr int NS = FP8 ? 3 : D == 64 ? 8 : 4;
     static constexpr int RS = FP8 ? 4 : 0;           // slots of E4M3 codes
     static constexpr int Q = 0;
@@ -80,11 +82,13 @@ struct Plan {
     static constexpr int ROWSCALE = RAW + RS * kSeg;
     static constexpr int ML = ROWSCALE + 512;
     static constexpr int BAR = ML + 1024;
-    // q_full, q_ready, full[NS], free[NS], v_ready[NS], raw_full[RS], raw_free[RS],
-    // per half s_full, p_full, pv_done, o_full; drain, b_done
-    static constexpr int NBAR = 2 + 3 * NS + 2 * RS + 8 + 2;
-    static constexpr int MISC = BAR + NBAR * 8;      // tensor memory address, abort flag,
-    static constexpr int BYTES = MISC + 160 + 1024;  // dirty range, ranges of 8 warps; alignment
+    // q_full, q_ready, full[NS], free[NS], raw_full[RS], raw_free[RS], per half
+    // s_full, p_full, pv_done, o_full; drain, b_done; per half and softmax warp
+    // the turn of its exponentials
+    static constexpr int NBAR = 2 + 2 * NS + 2 * RS + 8 + 2 + 8;
+    // tensor memory address, abort flag, dirty range, ranges of 8 warps, Stash
+    static constexpr int MISC = BAR + NBAR * 8;
+    static constexpr int BYTES = MISC + 192 + 1024;  // + alignment
     static_assert(BYTES <= 232448, "shared memory of one CTA");
     static constexpr int THREADS = FP8 ? 512 : 384;
     // setmaxnreg: softmax warps / the others.  The shares must fit what the
@@ -99,12 +103,20 @@ struct Ranges {
 };
 constexpr int kNoLo = INT_MAX, kNoHi = -1;
 
-// tanh(u / 2) = u * (c0 + c1 v + ... + c6 v^6), v = u^2, for |u| <= 2: a least
-// squares fit in v, reweighted towards the smallest largest relative error
-// (5e-8; 1.6e-7 in fp32 arithmetic).
-__device__ constexpr float kTanh[7] = {0.499999975f, -0.0416660489f, 0.00416412627f,
-                                       -0.000417633041f, 3.96288669e-05f, -3.02899346e-06f,
-                                       1.27077938e-07f};
+// tanh(u / 4) = u * (c0 + c1 v + c2 v^2 + ...), v = u^2: least squares fits in v,
+// reweighted towards the smallest largest relative error.  Four terms for
+// |u| <= 2 (6e-7 in fp32 arithmetic), seven for |u| <= 4 (1.6e-7); a
+// probability is rounded to 2^-9 or 2^-12 afterwards.
+__device__ constexpr float kTanh4[4] = {0.249999864f, -0.00520723718f, 0.00012881149f, -2.71009679e-06f};
+__device__ constexpr float kTanh7[7] = {0.249999988f, -0.00520825612f, 0.000130128946f,
+                                        -3.26275814e-06f, 7.74001316e-08f, -1.47900076e-09f,
+                                        1.55124447e-11f};
+
+// What the epilogue needs of the setup, kept in shared memory meanwhile (the
+// softmax loop needs the registers).
+struct Stash {
+    int q0, iA, g, part, parts, nt, kb, maxlo, minhi;
+};
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return fma2(a, b, make_float2(-0.f, -0.f));
@@ -145,13 +157,14 @@ template <int OT> __device__ __forceinline__ uint4 finite_only(const uint4& w) {
     return make_uint4(fix(w.x), fix(w.y), fix(w.z), fix(w.w));
 }
 
-// 8 E4M3 codes to 8 halves.
-__device__ __forceinline__ uint4 widen(uint32_t a, uint32_t b) {
-    auto two = [](uint32_t c) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3);
-        return (uint32_t)h.x | (uint32_t)h.y << 16;
-    };
-    return make_uint4(two(a & 0xffffu), two(a >> 16), two(b & 0xffffu), two(b >> 16));
+// Four E4M3 codes to four halves (exact).
+__device__ __forceinline__ uint2 widen(uint32_t codes) {
+    uint2 h;
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+        : "=r"(h.x), "=r"(h.y)
+        : "r"(codes));
+    return h;
 }
 
 // Row r of a swizzled bf16 query tile to f16, in place, times a power of two
@@ -192,6 +205,12 @@ template <int DT> __device__ __forceinline__ float cache_value(const void* p, si
     }
 }
 
+// tanh(u / 4) on the special-function unit: 1 - 2 / (1 + e^(u / 2)); past 2^30
+// that is 1 in fp32.
+__device__ __forceinline__ float tanh_quarter(float u) {
+    return fmaf(-2.f, rcp(1.f + ex2(min_nan(u * (0.5f * kLog2e), 30.f))), 1.f);
+}
+
 // Bits a..b (inclusive, any integers) of 32-bit word g.
 __device__ __forceinline__ uint32_t range_word(int a, int b, int g) {
     a -= 32 * g;
@@ -199,6 +218,17 @@ __device__ __forceinline__ uint32_t range_word(int a, int b, int g) {
     if (b < 0 || a > 31 || a > b) return 0u;
     const uint32_t up = b >= 31 ? ~0u : (2u << b) - 1u;
     return a <= 0 ? up : up & (~0u << a);
+}
+
+// 32 outputs o * f from element `at` on.
+template <int QT> __device__ __forceinline__ void store32(void* out, size_t at, const float* o, float f) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at * 2);
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        dst[v] = make_uint4(pack2<QT>(o[8 * v + 0] * f, o[8 * v + 1] * f),
+                            pack2<QT>(o[8 * v + 2] * f, o[8 * v + 3] * f),
+                            pack2<QT>(o[8 * v + 4] * f, o[8 * v + 5] * f),
+                            pack2<QT>(o[8 * v + 6] * f, o[8 * v + 7] * f));
 }
 
 // One sequence's new tokens, checked: false (and nothing to do) where they are
@@ -252,19 +282,20 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
     const uint32_t q_full = bar0, q_ready = bar0 + 8;
     auto full = [&](int i) { return bar0 + 8u * (2 + i); };
     auto free_ = [&](int i) { return bar0 + 8u * (2 + NS + i); };
-    auto v_ready = [&](int i) { return bar0 + 8u * (2 + 2 * NS + i); };
-    auto raw_full = [&](int i) { return bar0 + 8u * (2 + 3 * NS + i); };
-    auto raw_free = [&](int i) { return bar0 + 8u * (2 + 3 * NS + RS + i); };
-    const uint32_t bx = bar0 + 8u * (2 + 3 * NS + 2 * RS);
+    auto raw_full = [&](int i) { return bar0 + 8u * (2 + 2 * NS + i); };
+    auto raw_free = [&](int i) { return bar0 + 8u * (2 + 2 * NS + RS + i); };
+    const uint32_t bx = bar0 + 8u * (2 + 2 * NS + 2 * RS);
     auto s_full = [&](int x) { return bx + 8u * x; };
     auto p_full = [&](int x) { return bx + 8u * (2 + x); };
     auto pv_done = [&](int x) { return bx + 8u * (4 + x); };
     auto o_full = [&](int x) { return bx + 8u * (6 + x); };
     const uint32_t drain = bx + 64u, b_done = bx + 72u;
+    auto turn = [&](int x, int w) { return bx + 80u + 8u * (4 * x + w); };
     volatile int* misc = reinterpret_cast<volatile int*>(sm + L::MISC);
     volatile int* abort_flag = misc + 1;
     int* dirty = reinterpret_cast<int*>(sm + L::MISC) + 2;     // first, last tile with zeroed values
     int* wr = reinterpret_cast<int*>(sm + L::MISC) + 4;        // 8 warps x Ranges
+    volatile Stash* stash = reinterpret_cast<volatile Stash*>(sm + L::MISC + 144);
     float2* ml_b = reinterpret_cast<float2*>(sm + L::ML);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -301,7 +332,6 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         for (int i = 0; i < NS; ++i) {
             mbar_init(full(i), FP8 ? 4 : 1);
             mbar_init(free_(i), users);
-            mbar_init(v_ready(i), 1);
         }
         for (int i = 0; i < RS; ++i) {
             mbar_init(raw_full(i), 1);
@@ -315,6 +345,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         }
         mbar_init(drain, 2);
         mbar_init(b_done, 128);
+        for (int i = 0; i < 8; ++i) mbar_init(turn(i >> 2, i & 3), 1);
         misc[1] = 0;
         dirty[0] = INT_MAX;
         dirty[1] = -1;
@@ -345,21 +376,11 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
     const int hq = g * p.G + (r & (p.G - 1));              // query head of this thread's row
     const size_t out_row = (size_t)(q0 + it) * p.Hq + hq;
 
-    // store one row's 32 outputs, or its record's
-    auto store = [&](int c4, const float* o, float f) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + out_row * (size_t)(D * 2) + c4 * 64);
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-            dst[v] = make_uint4(pack2<QT>(o[8 * v + 0] * f, o[8 * v + 1] * f),
-                                pack2<QT>(o[8 * v + 2] * f, o[8 * v + 3] * f),
-                                pack2<QT>(o[8 * v + 4] * f, o[8 * v + 5] * f),
-                                pack2<QT>(o[8 * v + 6] * f, o[8 * v + 7] * f));
-    };
     const bool writes = row_ok && (hasB || warp < 4);
     if (nt == 0) {                                         // CTA-uniform: no key for any row
         if (writes && parts == 1 && part == 0) {
             const float zero[32] = {};
-            for (int c4 = 0; c4 < D / 32; ++c4) store(c4, zero, 0.f);
+            for (int c4 = 0; c4 < D / 32; ++c4) store32<QT>(p.out, out_row * D + c4 * 32, zero, 0.f);
         }
         if (writes && p.max_parts > 1)
             p.ws_ml[out_row * p.max_parts + part] = make_float2(-INFINITY, parts == 1 && part == 0 ? -1.f : 0.f);
@@ -379,6 +400,17 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
     // some row of the CTA does not see all keys of tile j
     auto masked = [&](int j) { return kb + j * kBN < maxlo_c || kb + j * kBN + kBN - 1 > minhi_c; };
 
+    if (threadIdx.x == 0) {
+        stash->q0 = q0;
+        stash->iA = iA;
+        stash->g = g;
+        stash->part = part;
+        stash->parts = parts;
+        stash->nt = nt;
+        stash->kb = kb;
+        stash->maxlo = maxlo_c;
+        stash->minhi = minhi_c;
+    }
     if (warp == 9) {
         tmem_alloc(sb + L::MISC, kTmemCols);
         tmem_relinquish();
@@ -486,9 +518,23 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             }
             __syncwarp();
             if (!(ok = warp_wait(full(sv), phase(2 * j + 1), abort_flag, p.err, 9))) break;
-            if constexpr (!FP8)
-                if (!(ok = warp_wait(v_ready(sv), phase(2 * j + 1), abort_flag, p.err, 9))) break;
             if (act) {
+                if (!FP8 && masked(j)) {
+                    // with B both warps look at (and mend) the whole tile, alike
+                    uint4* tile = reinterpret_cast<uint4*>(sm + L::OP + sv * L::TILE);
+                    bool bad = false;
+#pragma unroll 8
+                    for (int v = lane; v < L::TILE / 16; v += 32) bad |= nonfinite<OT>(tile[v]);
+                    if (__any_sync(~0u, bad)) {
+                        for (int v = lane; v < L::TILE / 16; v += 32) tile[v] = finite_only<OT>(tile[v]);
+                        if (lane == 0) {
+                            atomicMin(dirty, j);
+                            atomicMax(dirty + 1, j);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
                 if (!(ok = warp_wait(p_full(x), i & 1, abort_flag, p.err, 13))) break;
                 tc_fence_after();
                 if (lane == 0) {
@@ -513,31 +559,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         __syncwarp();
         warp_wait(drain, 0, abort_flag, p.err, 16, false);
     } else if (warp == 11) {
-        // -------------------------------------- 16-bit: the look through V
         regs_dec<L::ROTHER>();
-        if constexpr (!FP8) {
-            for (int j = 0; j < nt; ++j) {
-                const int u = 2 * j + 1, sv = slot(u);
-                if (!warp_wait(full(sv), phase(u), abort_flag, p.err, 9)) break;
-                if (masked(j)) {
-                    uint4* tile = reinterpret_cast<uint4*>(sm + L::OP + sv * L::TILE);
-                    bool bad = false;
-#pragma unroll 8
-                    for (int i = lane; i < L::TILE / 16; i += 32) bad |= nonfinite<OT>(tile[i]);
-                    if (__any_sync(~0u, bad)) {
-                        for (int i = lane; i < L::TILE / 16; i += 32) tile[i] = finite_only<OT>(tile[i]);
-                        if (lane == 0) {
-                            atomicMin(dirty, j);
-                            atomicMax(dirty + 1, j);
-                        }
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive(v_ready(sv));
-                __syncwarp();
-            }
-        }
     } else if (warp >= 12) {
         // ------------------------------------------- E4M3 codes to f16 operands
         regs_dec<L::ROTHER>();
@@ -558,7 +580,8 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                     // two in the other order, so a store meets every bank once.
                     const int t = i >> 3, ch = i & 7;
                     const uint4 w = *reinterpret_cast<const uint4*>(src + swz128(t, ch));
-                    uint4 a = widen(w.x, w.y), b = widen(w.z, w.w);
+                    const uint2 h0 = widen(w.x), h1 = widen(w.y), h2 = widen(w.z), h3 = widen(w.w);
+                    uint4 a = make_uint4(h0.x, h0.y, h1.x, h1.y), b = make_uint4(h2.x, h2.y, h3.x, h3.y);
                     if (look && (nonfinite<PA_F16>(a) || nonfinite<PA_F16>(b))) {
                         a = finite_only<PA_F16>(a);
                         b = finite_only<PA_F16>(b);
@@ -605,6 +628,20 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         }
         const float slope = BIAS && row_ok ? p.slopes[hq] * kLog2e : 0.f;
         const bool live = __any_sync(~0u, row_ok);         // a warp without rows only keeps step
+        // tiles [ja, jb) need no mask in this warp
+        const int ja = mine.maxlo <= kb ? 0 : ((min(mine.maxlo, INT_MAX - kBN) - kb - 1) >> 7) + 1;
+        const int jb = mine.minhi == INT_MAX ? INT_MAX : mine.minhi < kb ? 0 : (mine.minhi - kb + 1) >> 7;
+        // The turns: tiles [jt, jt + nturn) of A and B alternate (without B the
+        // even and the odd tiles), where this warp and its partner both have rows.
+        int jt = first, nturn = nt / 2;
+        if (hasB) {
+            int fo, eo;
+            span(x ? ra : rb, fo, eo);
+            jt = max(f, fo);
+            const bool partner = iB + (((warp & 3) * 32) >> p.log2G) < Ls;
+            nturn = partner ? min(e, eo) - jt : 0;
+        }
+        const uint32_t my_turn = turn(x, warp & 3), next_turn = turn(x ^ 1, warp & 3);
         int i = 0;                                         // tiles done
         for (int j = first; j < end && ok; j += step, ++i) {
             if (!(ok = warp_wait(s_full(x), i & 1, abort_flag, p.err, 12))) break;
@@ -613,30 +650,38 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                 continue;
             }
             tc_fence_after();
-            const int k0 = kb + j * kBN;
+            const bool mask = j < ja || j >= jb;
             float sv[kBN];
 #pragma unroll
             for (int c4 = 0; c4 < kBN / 32; ++c4) tmem_ld32(tS(x) + lrow + c4 * 32, sv + c4 * 32);
             tmem_wait_ld();
-            if constexpr (CAP || BIAS) {
-                const float2 sl2 = make_float2(sl, sl);
-                if constexpr (CAP) {
-                    // u = 2 scale x / softcap (sl), z = cap_log2 * tanh(u / 2): the
-                    // fit where no |u| of the warp reaches 2 (the second highest bit
-                    // of a float is set from 2 on, also of infinities and NaN)
-                    uint32_t big = 0u;
+            const float2 sl2 = make_float2(sl, sl);
+            // Scores in log2 units.  With a cap u = 4 scale x / softcap (the factor
+            // sl), z = cap_log2 * tanh(u / 4).  `fit`: no |u| of the warp reaches 2
+            // (the second highest bit of a float is set from 2 on, also of
+            // infinities and NaN) and no row masks: then sv keeps u, the row's
+            // maximum is tanh of the largest u, and the four-term fit runs with the
+            // exponentials below.
+            bool fit = false;
+            if constexpr (CAP) {
+                uint32_t big = 0u;
 #pragma unroll
-                    for (int k = 0; k < kBN; k += 2) {
-                        const float2 u = mul2(make_float2(sv[k], sv[k + 1]), sl2);
-                        sv[k] = u.x;
-                        sv[k + 1] = u.y;
-                        big |= __float_as_uint(u.x) | __float_as_uint(u.y);
-                    }
-                    if (!__any_sync(~0u, big & 0x40000000u)) {
-                        const float cl = p.cap_log2;
+                for (int k = 0; k < kBN; k += 2) {
+                    const float2 u = mul2(make_float2(sv[k], sv[k + 1]), sl2);
+                    sv[k] = u.x;
+                    sv[k + 1] = u.y;
+                    big |= __float_as_uint(u.x) | __float_as_uint(u.y);
+                }
+                fit = !BIAS && !mask && !__any_sync(~0u, big & 0x40000000u);
+                if (!fit) {
+                    const float cl = p.cap_log2;
+                    float top = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kBN; k += 2) top = max3(top, fabsf(sv[k]), fabsf(sv[k + 1]));
+                    if (!__any_sync(~0u, !(top <= 4.f))) {
                         float2 co[7];
 #pragma unroll
-                        for (int t = 0; t < 7; ++t) co[t] = make_float2(kTanh[t] * cl, kTanh[t] * cl);
+                        for (int t = 0; t < 7; ++t) co[t] = make_float2(kTanh7[t] * cl, kTanh7[t] * cl);
 #pragma unroll
                         for (int k = 0; k < kBN; k += 2) {
                             const float2 u = make_float2(sv[k], sv[k + 1]);
@@ -649,31 +694,26 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                             sv[k + 1] = y.y;
                         }
                     } else {
-                        // tanh(u / 2) = 1 - 2 / (1 + e^u); past e^u = 2^30 it is 1 in fp32
-                        const float cl = p.cap_log2;
 #pragma unroll
-                        for (int k = 0; k < kBN; ++k)
-                            sv[k] = fmaf(-2.f * cl, rcp(1.f + ex2(min_nan(sv[k] * kLog2e, 30.f))), cl);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < kBN; k += 2) {
-                        const float2 z = mul2(make_float2(sv[k], sv[k + 1]), sl2);
-                        sv[k] = z.x;
-                        sv[k + 1] = z.y;
+                        for (int k = 0; k < kBN; ++k) sv[k] = cl * tanh_quarter(sv[k]);
                     }
                 }
-                if constexpr (BIAS) {
-                    // distances as exact small integers (|i - p| past p: keys of a
-                    // prefix ahead of the row)
-                    const float d0 = (float)(pos - k0);
-                    const float2 ns = make_float2(-slope, -slope);
-                    const bool ahead = p.prefix_lens != nullptr;
+            }
+            if constexpr (BIAS) {
+                const float d0 = (float)(pos - (kb + j * kBN));      // distance of key 0
+                if (p.prefix_lens || fabsf(slope) > 64.f) {
+                    // distances as exact small integers (|i - p|: keys of a prefix
+                    // ahead of the row; slopes whose products lose what matters)
+#pragma unroll
+                    for (int k = 0; k < kBN; ++k)
+                        sv[k] = fmaf(-slope, fabsf(d0 - (float)k), CAP ? sv[k] : sv[k] * sl);
+                } else {
+                    const float b0 = -slope * d0;
 #pragma unroll
                     for (int k = 0; k < kBN; k += 2) {
-                        float2 d = add2(make_float2(d0, d0), make_float2(-(float)k, -(float)(k + 1)));
-                        if (ahead) d = make_float2(fabsf(d.x), fabsf(d.y));
-                        const float2 z = fma2(ns, d, make_float2(sv[k], sv[k + 1]));
+                        const float2 b = make_float2(fmaf(slope, (float)k, b0), fmaf(slope, (float)(k + 1), b0));
+                        const float2 z = CAP ? add2(make_float2(sv[k], sv[k + 1]), b)
+                                             : fma2(make_float2(sv[k], sv[k + 1]), sl2, b);
                         sv[k] = z.x;
                         sv[k + 1] = z.y;
                     }
@@ -681,7 +721,8 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             }
             // keys outside a row's range become -inf; a tile that no row of the
             // warp masks skips the compares
-            if (k0 < mine.maxlo || k0 + kBN - 1 > mine.minhi) {
+            if (mask) {
+                const int k0 = kb + j * kBN;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const uint32_t bits = range_word(lo == kNoLo ? kBN : lo - k0, hi - k0, w);
@@ -699,6 +740,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             float tmax = fmaxf(max3(pm[0], pm[1], pm[2]),
                                fmaxf(max3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])));
             if constexpr (!CAP && !BIAS) tmax *= sl;           // scale > 0
+            if (CAP && !BIAS && fit) tmax = p.cap_log2 * tanh_quarter(tmax);
             const float m_new = fmaxf(m_use, tmax);
             const bool raise = m_new > m_use + kRescaleLog2;
             const float alpha = raise ? ex2(m_use - m_new) : 1.f;
@@ -719,25 +761,49 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                 }
                 tmem_wait_st();
             }
+            const int at = hasB ? j - jt : i;                  // this tile's turn
+            if (x ? at >= 0 && at < nturn : at > 0 && at <= nturn)
+                if (!(ok = warp_wait(my_turn, (at - 1 + x) & 1, abort_flag, p.err, 19))) break;
             // probabilities, rounded to the operand type, two per 32-bit column
             // over the scores they came from; a row that has seen no key yet has
             // no maximum to take off.  f16 operands are 2^7 times as large (at most
             // 2^15), so that small ones keep their bits; l carries the same factor.
             const float nm = (OT == PA_F16 ? 7.f : 0.f) - (m_use == -INFINITY ? 0.f : m_use);
-            const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(nm, nm);
+            const float2 nm2 = make_float2(nm, nm);
+            auto exponentials = [&](auto arg) {
 #pragma unroll
-            for (int c16 = 0; c16 < kBN / 32; ++c16) {
-                uint32_t w[16];
+                for (int c16 = 0; c16 < kBN / 32; ++c16) {
+                    uint32_t w[16];
 #pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    const int k = c16 * 32 + 2 * v;
-                    const float2 z = make_float2(sv[k], sv[k + 1]);
-                    const float2 d = CAP || BIAS ? add2(z, nm2) : fma2(z, sl2, nm2);
-                    sv[k] = ex2(d.x);
-                    sv[k + 1] = ex2(d.y);
-                    w[v] = pack2<OT>(sv[k], sv[k + 1]);
+                    for (int v = 0; v < 16; ++v) {
+                        const int k = c16 * 32 + 2 * v;
+                        const float2 d = arg(make_float2(sv[k], sv[k + 1]));
+                        sv[k] = ex2(d.x);
+                        sv[k + 1] = ex2(d.y);
+                        w[v] = pack2<OT>(sv[k], sv[k + 1]);
+                    }
+                    tmem_st16(tS(x) + lrow + c16 * 16, w);
                 }
-                tmem_st16(tS(x) + lrow + c16 * 16, w);
+            };
+            if constexpr (!CAP && !BIAS) {
+                exponentials([&](float2 z) { return fma2(z, sl2, nm2); });
+            } else {
+                if (CAP && !BIAS && fit) {
+                    const float cl = p.cap_log2;
+                    float2 co[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) co[t] = make_float2(kTanh4[t] * cl, kTanh4[t] * cl);
+                    exponentials([&](float2 u) {
+                        const float2 v = mul2(u, u);
+                        return fma2(u, fma2(fma2(fma2(co[3], v, co[2]), v, co[1]), v, co[0]), nm2);
+                    });
+                } else {
+                    exponentials([&](float2 z) { return add2(z, nm2); });
+                }
+            }
+            if (at >= 0 && at < nturn) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(next_turn);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -751,15 +817,16 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                     ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
         }
         // -------------------------------------------------------- epilogue
-        float fa = 1.f, fb = 0.f;                          // weights of O_A / O_X and O_B
-        bool has_o = i > 0;                                // the half's O was written
+        float fa = 1.f, fb = 0.f;                          // weights of O_X and O_B
+        const bool has_o = i > 0;                          // the half's O was written
         if (ok && has_o) ok = warp_wait(o_full(x), 0, abort_flag, p.err, 15);
+        const int ntiles = stash->nt;
         if (!hasB) {
             if (x == 1) {
                 ml_b[r] = make_float2(m_use, lsum);
                 mbar_arrive(b_done);
                 ok = false;                                // half A writes the rows
-            } else if (ok && nt > 1) {
+            } else if (ok && ntiles > 1) {
                 ok = warp_wait(b_done, 0, abort_flag, p.err, 18) &&
                      warp_wait(o_full(1), 0, abort_flag, p.err, 15);
                 const float2 b = ml_b[r];
@@ -773,10 +840,13 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         }
         if (ok && live) {
             tc_fence_after();
-            const bool record = parts > 1;
+            const int g = stash->g, part = stash->part, kb = stash->kb;
+            const int it = stash->iA + (hasB && x ? p.TQ : 0) + (r >> p.log2G);
+            const size_t out_row = (size_t)(stash->q0 + it) * p.Hq + g * p.G + (r & (p.G - 1));
+            const bool record = stash->parts > 1;
             const float inv = record ? 1.f : lsum == 0.f ? 0.f : p.v_scale / lsum;
             const bool fix = dirty[1] >= 0;                // values were taken out of V
-            const bool both = !hasB && nt > 1;
+            const bool both = !hasB && ntiles > 1;
 #pragma unroll 1
             for (int c4 = 0; c4 < D / 32; ++c4) {
                 float o[32];
@@ -794,12 +864,13 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
 #pragma unroll
                     for (int v = 0; v < 32; ++v) o[v] = o[v] * fa + ob[v] * fb;
                 }
-                if (fix && row_ok) {
+                if (fix && row_ok && lo != kNoLo) {
                     const int ka = max(lo, kb + dirty[0] * kBN);
                     const int kz = min(hi, kb + dirty[1] * kBN + kBN - 1);
-                    for (int k = ka; k <= kz && lo != kNoLo; ++k) {
-                        if (!masked((k - kb) >> 7)) {      // this tile kept its values
-                            k = kb + ((k - kb) | (kBN - 1));
+                    for (int k = ka; k <= kz; ++k) {
+                        const int k0 = k - ((k - kb) & (kBN - 1));
+                        if (k0 >= stash->maxlo && k0 + kBN - 1 <= stash->minhi) {
+                            k = k0 + kBN - 1;              // this tile kept its values
                             continue;
                         }
                         const int id = p.block_tables[(size_t)s * p.MB + (k >> p.log2bs)];
@@ -819,7 +890,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                         for (int v = 0; v < 8; ++v)
                             dst[v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
                     } else {
-                        store(c4, o, inv);
+                        store32<QT>(p.out, out_row * D + c4 * 32, o, inv);
                     }
                 }
             }

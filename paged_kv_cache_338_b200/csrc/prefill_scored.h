@@ -24,7 +24,7 @@ struct Params {
     int T, Hq, G, log2G, TQ, MB, bs, log2bs, max_qlen, max_ctx, n_pairs, pair_group;
     int window;                   // > 0: keys at distance >= window are not visible
     int part_tiles, max_parts;    // key tiles per part; parts of a row at most
-    float sl;                     // scale * k_scale * log2 e, with a cap 2 * scale * k_scale / softcap
+    float sl;                     // scale * k_scale * log2 e, with a cap 4 * scale * k_scale / softcap
     float cap_log2;               // softcap * log2 e, 0: none
     float v_scale;
     float2* ws_ml;                // [T, Hq, max_parts] (m, l)
