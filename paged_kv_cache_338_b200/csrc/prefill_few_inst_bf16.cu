@@ -1,0 +1,6 @@
+// Instantiations of the few-row chunk attention: bf16 queries and cache.
+#include "prefill_few.cuh"
+
+cudaError_t ps::launch_few_bf16(const Launch& a, int D) {
+    return D == 64 ? launch_few<PA_BF16, false, 64>(a) : launch_few<PA_BF16, false, 128>(a);
+}

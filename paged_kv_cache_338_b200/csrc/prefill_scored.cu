@@ -28,6 +28,12 @@ int64_t parts_of(int max_query_len, int max_ctx, int window, int partition) {
     return std::max<int64_t>(1, (span_of(max_query_len, max_ctx, window) + partition - 1) / partition);
 }
 
+// Columns of the few-row kernel that hold the rows of a kv head, 0: too many.
+int rows_of(int max_query_len, int G) {
+    const int64_t rows = (int64_t)max_query_len * G;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
+}
+
 pa_status check_sizes(int max_query_len, int max_ctx, int window, int partition) {
     if (max_query_len < 0 || max_ctx < 0 || window < 0 || partition < 0)
         return fail(PA_ERR_INVALID_ARG, "negative size");
@@ -119,8 +125,10 @@ extern "C" pa_status pa_prefill_scored(
     if (!pa::aligned16(out) || !pa::aligned16(q) || !pa::aligned16(key_cache) ||
         !pa::aligned16(value_cache))
         return fail(PA_ERR_INVALID_ARG, "out, q and the caches must be 16-byte aligned");
-    const int TQ = kRows / G;
-    const int64_t n_pairs = ((int64_t)max_query_len + 2 * TQ - 1) / (2 * TQ);
+    // few rows of a kv head: the kernel whose MMA columns are the queries
+    const int few = rows_of(max_query_len, G);
+    const int TQ = (few ? few : kRows) / G;
+    const int64_t n_pairs = few ? 1 : ((int64_t)max_query_len + 2 * TQ - 1) / (2 * TQ);
     const int64_t parts = parts_of(max_query_len, max_ctx, window, partition);
     // as many pair slots per group as there are pairs: a CTA that only exits
     // would hold a whole SM's shared memory for a moment
@@ -182,10 +190,16 @@ extern "C" pa_status pa_prefill_scored(
     a.mk = &mk;
     a.mv = &mv;
     a.p = &p;
+    a.few = few;
     a.grid = dim3((unsigned)(Hkv * pair_group * parts), (unsigned)S, (unsigned)groups);
     a.stream = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = fp8 ? (q_dt == PA_BF16 ? ps::launch_fp8_q_bf16(a, D) : ps::launch_fp8_q_f16(a, D))
-                              : (q_dt == PA_BF16 ? ps::launch_bf16(a, D) : ps::launch_f16(a, D));
+    cudaError_t e;
+    if (few)
+        e = fp8 ? (q_dt == PA_BF16 ? ps::launch_few_fp8_q_bf16(a, D) : ps::launch_few_fp8_q_f16(a, D))
+                : (q_dt == PA_BF16 ? ps::launch_few_bf16(a, D) : ps::launch_few_f16(a, D));
+    else
+        e = fp8 ? (q_dt == PA_BF16 ? ps::launch_fp8_q_bf16(a, D) : ps::launch_fp8_q_f16(a, D))
+                : (q_dt == PA_BF16 ? ps::launch_bf16(a, D) : ps::launch_f16(a, D));
     if (e != cudaSuccess) return pa::cuda_fail(e, "scored prefill launch");
     return PA_OK;
 }

@@ -119,7 +119,35 @@ struct Stash {
 };
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    return fma2(a, b, make_float2(-0.f, -0.f));
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// fma2 and mul2 that stay in the order they are written in: neighbours that share
+// an operand read it once (a packed FMA of three fresh register pairs takes 3
+// cycles, not 2).
+__device__ __forceinline__ float2 fma2_here(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm volatile("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2_here(float2 a, float2 b) {
+    float2 d;
+    asm volatile("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 
 // 1 / x on the special-function unit (1 / infinity = 0).
@@ -169,13 +197,13 @@ __device__ __forceinline__ uint2 widen(uint32_t codes) {
 
 // Row r of a swizzled bf16 query tile to f16, in place, times a power of two
 // that sets its largest element to 2^14..2^15; returns the inverse.
-template <int D> __device__ __forceinline__ float row_to_f16(uint8_t* tile, int r) {
+template <int D, int SEG = kSeg> __device__ __forceinline__ float row_to_f16(uint8_t* tile, int r) {
     constexpr int N = D / 8;
     uint4 w[N];
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        w[i] = *reinterpret_cast<const uint4*>(tile + (i >> 3) * kSeg + swz128(r, i & 7));
+        w[i] = *reinterpret_cast<const uint4*>(tile + (i >> 3) * SEG + swz128(r, i & 7));
         float f[8];
         Chunk<PA_BF16>::to_float(w[i], f);
 #pragma unroll
@@ -188,7 +216,7 @@ template <int D> __device__ __forceinline__ float row_to_f16(uint8_t* tile, int 
     for (int i = 0; i < N; ++i) {
         float f[8];
         Chunk<PA_BF16>::to_float(w[i], f);
-        *reinterpret_cast<uint4*>(tile + (i >> 3) * kSeg + swz128(r, i & 7)) =
+        *reinterpret_cast<uint4*>(tile + (i >> 3) * SEG + swz128(r, i & 7)) =
             make_uint4(pack2<PA_F16>(f[0] * up, f[1] * up), pack2<PA_F16>(f[2] * up, f[3] * up),
                        pack2<PA_F16>(f[4] * up, f[5] * up), pack2<PA_F16>(f[6] * up, f[7] * up));
     }
@@ -664,14 +692,15 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             // exponentials below.
             bool fit = false;
             if constexpr (CAP) {
-                uint32_t big = 0u;
+                uint32_t bits[8] = {};                 // independent chains
 #pragma unroll
                 for (int k = 0; k < kBN; k += 2) {
                     const float2 u = mul2(make_float2(sv[k], sv[k + 1]), sl2);
                     sv[k] = u.x;
                     sv[k + 1] = u.y;
-                    big |= __float_as_uint(u.x) | __float_as_uint(u.y);
+                    bits[(k >> 1) & 7] |= __float_as_uint(u.x) | __float_as_uint(u.y);
                 }
+                const uint32_t big = ((bits[0] | bits[1] | bits[2]) | (bits[3] | bits[4] | bits[5])) | bits[6] | bits[7];
                 fit = !BIAS && !mask && !__any_sync(~0u, big & 0x40000000u);
                 if (!fit) {
                     const float cl = p.cap_log2;
@@ -761,45 +790,64 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                 }
                 tmem_wait_st();
             }
-            const int at = hasB ? j - jt : i;                  // this tile's turn
-            if (x ? at >= 0 && at < nturn : at > 0 && at <= nturn)
-                if (!(ok = warp_wait(my_turn, (at - 1 + x) & 1, abort_flag, p.err, 19))) break;
             // probabilities, rounded to the operand type, two per 32-bit column
             // over the scores they came from; a row that has seen no key yet has
             // no maximum to take off.  f16 operands are 2^7 times as large (at most
             // 2^15), so that small ones keep their bits; l carries the same factor.
             const float nm = (OT == PA_F16 ? 7.f : 0.f) - (m_use == -INFINITY ? 0.f : m_use);
             const float2 nm2 = make_float2(nm, nm);
-            auto exponentials = [&](auto arg) {
+            // the fit runs on the FMA pipe beside the partner warp's exponentials
+            if (CAP && !BIAS && fit) {
+                const float cl = p.cap_log2;
+                float2 co[4];
 #pragma unroll
-                for (int c16 = 0; c16 < kBN / 32; ++c16) {
-                    uint32_t w[16];
+                for (int t = 0; t < 4; ++t) co[t] = make_float2(kTanh4[t] * cl, kTanh4[t] * cl);
+                constexpr int N = 4;                    // pairs worked on side by side
 #pragma unroll
-                    for (int v = 0; v < 16; ++v) {
-                        const int k = c16 * 32 + 2 * v;
-                        const float2 d = arg(make_float2(sv[k], sv[k + 1]));
-                        sv[k] = ex2(d.x);
-                        sv[k + 1] = ex2(d.y);
-                        w[v] = pack2<OT>(sv[k], sv[k + 1]);
+                for (int k = 0; k < kBN; k += 2 * N) {
+                    float2 v[N], y[N];
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const float2 u = make_float2(sv[k + 2 * e], sv[k + 2 * e + 1]);
+                        v[e] = mul2_here(u, u);
                     }
-                    tmem_st16(tS(x) + lrow + c16 * 16, w);
-                }
-            };
-            if constexpr (!CAP && !BIAS) {
-                exponentials([&](float2 z) { return fma2(z, sl2, nm2); });
-            } else {
-                if (CAP && !BIAS && fit) {
-                    const float cl = p.cap_log2;
-                    float2 co[4];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) co[t] = make_float2(kTanh4[t] * cl, kTanh4[t] * cl);
-                    exponentials([&](float2 u) {
-                        const float2 v = mul2(u, u);
-                        return fma2(u, fma2(fma2(fma2(co[3], v, co[2]), v, co[1]), v, co[0]), nm2);
-                    });
-                } else {
-                    exponentials([&](float2 z) { return add2(z, nm2); });
+                    for (int e = 0; e < N; ++e) y[e] = fma2_here(co[3], v[e], co[2]);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) y[e] = fma2_here(y[e], v[e], co[1]);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) y[e] = fma2_here(y[e], v[e], co[0]);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        y[e] = fma2_here(make_float2(sv[k + 2 * e], sv[k + 2 * e + 1]), y[e], nm2);
+                        sv[k + 2 * e] = y[e].x;
+                        sv[k + 2 * e + 1] = y[e].y;
+                    }
                 }
+            } else if constexpr (CAP || BIAS) {
+#pragma unroll
+                for (int k = 0; k < kBN; k += 2) {
+                    const float2 d = add2(make_float2(sv[k], sv[k + 1]), nm2);
+                    sv[k] = d.x;
+                    sv[k + 1] = d.y;
+                }
+            }
+            const int at = hasB ? j - jt : i;                  // this tile's turn
+            if (x ? at >= 0 && at < nturn : at > 0 && at <= nturn)
+                if (!(ok = warp_wait(my_turn, (at - 1 + x) & 1, abort_flag, p.err, 19))) break;
+#pragma unroll
+            for (int c16 = 0; c16 < kBN / 32; ++c16) {
+                uint32_t w[16];
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int k = c16 * 32 + 2 * v;
+                    float2 d = make_float2(sv[k], sv[k + 1]);
+                    if constexpr (!CAP && !BIAS) d = fma2(d, sl2, nm2);
+                    sv[k] = ex2(d.x);
+                    sv[k + 1] = ex2(d.y);
+                    w[v] = pack2<OT>(sv[k], sv[k + 1]);
+                }
+                tmem_st16(tS(x) + lrow + c16 * 16, w);
             }
             if (at >= 0 && at < nturn) {
                 __syncwarp();
@@ -968,8 +1016,11 @@ cudaError_t launch_one(const Launch& a) {
         regs.store(have, std::memory_order_relaxed);
     }
     if (have * L::THREADS < L::RTOTAL) return cudaErrorInvalidConfiguration;
-    e = launch_pdl(kern, a.grid, dim3(L::THREADS), (size_t)L::BYTES, a.stream, *a.mq, *a.mk, *a.mv, *a.p);
-    if (e != cudaSuccess || a.p->max_parts == 1) return e;
+    return launch_pdl(kern, a.grid, dim3(L::THREADS), (size_t)L::BYTES, a.stream, *a.mq, *a.mk, *a.mv, *a.p);
+}
+
+template <int QT, int D> cudaError_t launch_merge(const Launch& a) {
+    if (a.p->max_parts == 1) return cudaSuccess;
     const unsigned rows = (unsigned)(((long long)a.p->max_qlen * a.p->Hq + 7) / 8);
     return launch_pdl(prefill_scored_merge<QT, D>, dim3(rows, a.grid.y), dim3(256), 0, a.stream, *a.p);
 }
@@ -977,8 +1028,10 @@ cudaError_t launch_one(const Launch& a) {
 template <int QT, bool FP8, int D>
 cudaError_t launch_mod(const Launch& a) {
     const bool cap = a.p->cap_log2 > 0.f, bias = a.p->slopes != nullptr;
-    if (cap) return bias ? launch_one<QT, FP8, D, true, true>(a) : launch_one<QT, FP8, D, true, false>(a);
-    return bias ? launch_one<QT, FP8, D, false, true>(a) : launch_one<QT, FP8, D, false, false>(a);
+    cudaError_t e;
+    if (cap) e = bias ? launch_one<QT, FP8, D, true, true>(a) : launch_one<QT, FP8, D, true, false>(a);
+    else e = bias ? launch_one<QT, FP8, D, false, true>(a) : launch_one<QT, FP8, D, false, false>(a);
+    return e == cudaSuccess ? launch_merge<QT, D>(a) : e;
 }
 
 }  // namespace ps

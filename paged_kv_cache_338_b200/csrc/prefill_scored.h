@@ -35,6 +35,7 @@ struct Launch {
     const CUtensorMap *mq, *mk, *mv;
     const Params* p;
     dim3 grid;
+    int few;                      // columns of the few-row kernel (16 or 32), 0: the other one
     cudaStream_t stream;
 };
 
@@ -42,5 +43,9 @@ cudaError_t launch_bf16(const Launch& a, int D);
 cudaError_t launch_f16(const Launch& a, int D);
 cudaError_t launch_fp8_q_bf16(const Launch& a, int D);
 cudaError_t launch_fp8_q_f16(const Launch& a, int D);
+cudaError_t launch_few_bf16(const Launch& a, int D);
+cudaError_t launch_few_f16(const Launch& a, int D);
+cudaError_t launch_few_fp8_q_bf16(const Launch& a, int D);
+cudaError_t launch_few_fp8_q_f16(const Launch& a, int D);
 
 }  // namespace ps
