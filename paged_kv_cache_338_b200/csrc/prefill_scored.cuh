@@ -197,28 +197,25 @@ __device__ __forceinline__ uint2 widen(uint32_t codes) {
 
 // Row r of a swizzled bf16 query tile to f16, in place, times a power of two
 // that sets its largest element to 2^14..2^15; returns the inverse.
-template <int D, int SEG = kSeg> __device__ __forceinline__ float row_to_f16(uint8_t* tile, int r) {
-    constexpr int N = D / 8;
-    uint4 w[N];
+template <int D, int SEG = kSeg> __device__ __forceinline__ float row_to_f16(uint32_t tile, int r) {
     float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        w[i] = *reinterpret_cast<const uint4*>(tile + (i >> 3) * SEG + swz128(r, i & 7));
+#pragma unroll 1
+    for (int i = 0; i < D / 8; ++i) {
         float f[8];
-        Chunk<PA_BF16>::to_float(w[i], f);
+        Chunk<PA_BF16>::to_float(lds128(tile + (i >> 3) * SEG + swz128(r, i & 7)), f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]));
     }
     int sh = 0;                        // rows of zeros, or with an infinity: as they are
     if (top > 0.f && top <= 3.4e38f) sh = min(126, 14 - ((int)(__float_as_uint(top) >> 23) - 127));
     const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < D / 8; ++i) {
+        const uint32_t at = tile + (i >> 3) * SEG + swz128(r, i & 7);
         float f[8];
-        Chunk<PA_BF16>::to_float(w[i], f);
-        *reinterpret_cast<uint4*>(tile + (i >> 3) * SEG + swz128(r, i & 7)) =
-            make_uint4(pack2<PA_F16>(f[0] * up, f[1] * up), pack2<PA_F16>(f[2] * up, f[3] * up),
-                       pack2<PA_F16>(f[4] * up, f[5] * up), pack2<PA_F16>(f[6] * up, f[7] * up));
+        Chunk<PA_BF16>::to_float(lds128(at), f);
+        sts128(at, make_uint4(pack2<PA_F16>(f[0] * up, f[1] * up), pack2<PA_F16>(f[2] * up, f[3] * up),
+                              pack2<PA_F16>(f[4] * up, f[5] * up), pack2<PA_F16>(f[6] * up, f[7] * up)));
     }
     return __uint_as_float((uint32_t)(127 - sh) << 23);
 }
@@ -288,7 +285,8 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
     const int PG = p.pair_group;
     const int unit = (int)blockIdx.x / PG;
     const int pair = ((int)gridDim.z - 1 - (int)blockIdx.z) * PG + (PG - 1 - (int)blockIdx.x % PG);
-    const int part = unit % p.max_parts, g = unit / p.max_parts;
+    const int heads = p.Hq >> p.log2G;
+    const int part = unit / heads, g = unit % heads;
     if (pair >= p.n_pairs) return;
     const int s = (int)blockIdx.y;
     int q0, Ls, n;
@@ -357,14 +355,17 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         const int users = hasB ? 2 : 1;                    // halves that read a slot
         mbar_init(q_full, 1);
         mbar_init(q_ready, hasB ? 256 : 128);
+#pragma unroll 1
         for (int i = 0; i < NS; ++i) {
             mbar_init(full(i), FP8 ? 4 : 1);
             mbar_init(free_(i), users);
         }
+#pragma unroll 1
         for (int i = 0; i < RS; ++i) {
             mbar_init(raw_full(i), 1);
             mbar_init(raw_free(i), 4);
         }
+#pragma unroll 1
         for (int x = 0; x < 2; ++x) {
             mbar_init(s_full(x), 1);
             mbar_init(p_full(x), 128);
@@ -373,6 +374,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         }
         mbar_init(drain, 2);
         mbar_init(b_done, 128);
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) mbar_init(turn(i >> 2, i & 3), 1);
         misc[1] = 0;
         dirty[0] = INT_MAX;
@@ -384,6 +386,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
     // the halves' ranges, and which key tiles this CTA takes
     auto half = [&](int x) {
         Ranges q = {kNoLo, -1, INT_MAX, kNoHi};
+#pragma unroll 1
         for (int w = 4 * x; w < 4 * x + 4; ++w) {
             q.minlo = min(q.minlo, wr[4 * w]);
             q.maxlo = max(q.maxlo, wr[4 * w + 1]);
@@ -408,6 +411,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
     if (nt == 0) {                                         // CTA-uniform: no key for any row
         if (writes && parts == 1 && part == 0) {
             const float zero[32] = {};
+#pragma unroll 1
             for (int c4 = 0; c4 < D / 32; ++c4) store32<QT>(p.out, out_row * D + c4 * 32, zero, 0.f);
         }
         if (writes && p.max_parts > 1)
@@ -460,7 +464,9 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         const uint32_t box = (uint32_t)p.bs * 128u;
         if (lane == 0) {
             mbar_arrive_expect_tx(q_full, (hasB ? 2 : 1) * L::TILE);
+#pragma unroll 1
             for (int x = 0; x < (hasB ? 2 : 1); ++x)
+#pragma unroll 1
                 for (int sg = 0; sg < NSEG; ++sg)
                     tma_load_3d(sQ + x * L::TILE + sg * kSeg, &tmq, q_full, sg * 64, g * p.G,
                                 q0 + (x ? iB : iA));
@@ -468,6 +474,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         constexpr int RING = FP8 ? RS : NS;
         constexpr uint32_t TX = FP8 ? kSeg : L::TILE;
         int started = 0;
+#pragma unroll 1
         for (int j = 0; j < nt; ++j) {
             const int lb = ((kb + j * kBN) >> p.log2bs) + lane;
             // a block past the last visible key, or an id outside the cache,
@@ -493,6 +500,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                         tma_load_4d_plain(sRAW + st * kSeg + lane * box, kv ? &tmv : &tmk, fb, 0, g,
                                           0, id);
                     } else {
+#pragma unroll 1
                         for (int sg = 0; sg < NSEG; ++sg)
                             tma_load_4d_plain(sOP + st * L::TILE + sg * kSeg + lane * box,
                                               kv ? &tmv : &tmk, fb, sg * 64, g, 0, id);
@@ -503,6 +511,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             if (!ok) break;
         }
         // every copy this warp started has landed before the CTA may exit
+#pragma unroll 1
         for (int i = 0; i < RING && i < started; ++i) {
             const int last = i + (started - 1 - i) / RING * RING;
             warp_wait(FP8 ? raw_full(i) : full(i), (last / RING) & 1, abort_flag, p.err, 17, false);
@@ -522,6 +531,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         const int last = hasB ? e - 1 : nt - 1 - ((nt - 1 - x) & 1);
         bool ok = warp_wait(QCONV ? q_ready : q_full, 0, abort_flag, p.err, 7);
         int i = 0;                                             // tiles done
+#pragma unroll 1
         for (int j = first; j < nt && ok; j += step) {
             const bool act = j >= f && j < e;
             const int sk = slot(2 * j), sv = slot(2 * j + 1);
@@ -549,12 +559,13 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             if (act) {
                 if (!FP8 && masked(j)) {
                     // with B both warps look at (and mend) the whole tile, alike
-                    uint4* tile = reinterpret_cast<uint4*>(sm + L::OP + sv * L::TILE);
+                    const uint32_t tile = sOP + sv * L::TILE + lane * 16;
                     bool bad = false;
 #pragma unroll 8
-                    for (int v = lane; v < L::TILE / 16; v += 32) bad |= nonfinite<OT>(tile[v]);
+                    for (int v = 0; v < L::TILE; v += 512) bad |= nonfinite<OT>(lds128(tile + v));
                     if (__any_sync(~0u, bad)) {
-                        for (int v = lane; v < L::TILE / 16; v += 32) tile[v] = finite_only<OT>(tile[v]);
+#pragma unroll 1
+                        for (int v = 0; v < L::TILE; v += 512) sts128(tile + v, finite_only<OT>(lds128(tile + v)));
                         if (lane == 0) {
                             atomicMin(dirty, j);
                             atomicMax(dirty + 1, j);
@@ -593,13 +604,12 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         regs_dec<L::ROTHER>();
         if constexpr (FP8) {
             const int tid = threadIdx.x - 384;
+#pragma unroll 1
             for (int u = 0; u < 2 * nt; ++u) {
                 const int rs = u % RS, st = slot(u);
                 if (!warp_wait(raw_full(rs), (u / RS) & 1, abort_flag, p.err, 9)) break;
                 if (!warp_wait(free_(st), phase(u) ^ 1, abort_flag, p.err, 10)) break;
-                const uint8_t* src = sm + L::RAW + rs * kSeg;
-                uint8_t* dst = sm + L::OP + st * L::TILE;
-                const bool look = (u & 1) && masked(u >> 1);
+                const uint32_t src = sRAW + rs * kSeg, dst = sOP + st * L::TILE;
                 bool bad = false;
 #pragma unroll 4
                 for (int i = tid; i < kBN * 8; i += 128) {
@@ -607,20 +617,22 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                     // operand segment ch / 4.  The lanes of segment 1 write their
                     // two in the other order, so a store meets every bank once.
                     const int t = i >> 3, ch = i & 7;
-                    const uint4 w = *reinterpret_cast<const uint4*>(src + swz128(t, ch));
+                    const uint4 w = lds128(src + swz128(t, ch));
                     const uint2 h0 = widen(w.x), h1 = widen(w.y), h2 = widen(w.z), h3 = widen(w.w);
-                    uint4 a = make_uint4(h0.x, h0.y, h1.x, h1.y), b = make_uint4(h2.x, h2.y, h3.x, h3.y);
-                    if (look && (nonfinite<PA_F16>(a) || nonfinite<PA_F16>(b))) {
-                        a = finite_only<PA_F16>(a);
-                        b = finite_only<PA_F16>(b);
-                        bad = true;
-                    }
-                    uint8_t* seg = dst + (ch >> 2) * kSeg;
+                    const uint4 a = make_uint4(h0.x, h0.y, h1.x, h1.y), b = make_uint4(h2.x, h2.y, h3.x, h3.y);
+                    bad |= nonfinite<PA_F16>(a) | nonfinite<PA_F16>(b);
+                    const uint32_t seg = dst + (ch >> 2) * kSeg;
                     const int oc = 2 * (ch & 3), sw = ch >> 2;
-                    *reinterpret_cast<uint4*>(seg + swz128(t, oc + sw)) = sw ? b : a;
-                    *reinterpret_cast<uint4*>(seg + swz128(t, oc + 1 - sw)) = sw ? a : b;
+                    sts128(seg + swz128(t, oc + sw), sw ? b : a);
+                    sts128(seg + swz128(t, oc + 1 - sw), sw ? a : b);
                 }
-                if (bad) {
+                if (bad && (u & 1) && masked(u >> 1)) {       // this thread's chunks once more
+#pragma unroll 1
+                    for (int i = 0; i < 16; ++i) {
+                        const int t = (tid >> 3) + 16 * (i >> 1), ch = tid & 7;
+                        const uint32_t at = dst + (ch >> 2) * kSeg + swz128(t, 2 * (ch & 3) + (i & 1));
+                        sts128(at, finite_only<PA_F16>(lds128(at)));
+                    }
                     atomicMin(dirty, u >> 1);
                     atomicMax(dirty + 1, u >> 1);
                 }
@@ -647,7 +659,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             float* rowscale = reinterpret_cast<float*>(sm + L::ROWSCALE);
             ok = warp_wait(q_full, 0, abort_flag, p.err, 7);
             if (ok && (hasB || x == 0)) {
-                rowscale[threadIdx.x] = row_to_f16<D>(sm + L::Q + x * L::TILE, r);
+                rowscale[threadIdx.x] = row_to_f16<D>(sQ + x * L::TILE, r);
                 fence_proxy_async_smem();
                 mbar_arrive(q_ready);
             }
@@ -671,6 +683,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         }
         const uint32_t my_turn = turn(x, warp & 3), next_turn = turn(x ^ 1, warp & 3);
         int i = 0;                                         // tiles done
+#pragma unroll 1
         for (int j = first; j < end && ok; j += step, ++i) {
             if (!(ok = warp_wait(s_full(x), i & 1, abort_flag, p.err, 12))) break;
             if (!live) {
@@ -915,6 +928,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                 if (fix && row_ok && lo != kNoLo) {
                     const int ka = max(lo, kb + dirty[0] * kBN);
                     const int kz = min(hi, kb + dirty[1] * kBN + kBN - 1);
+#pragma unroll 1
                     for (int k = ka; k <= kz; ++k) {
                         const int k0 = k - ((k - kb) & (kBN - 1));
                         if (k0 >= stash->maxlo && k0 + kBN - 1 <= stash->minhi) {
@@ -969,6 +983,7 @@ __global__ void __launch_bounds__(256) prefill_scored_merge(const Params p) {
     const float2* ml = p.ws_ml + row * p.max_parts;
     if (ml[0].y == -1.f) return;                           // written by the attention kernel
     float m = -INFINITY;
+#pragma unroll 1
     for (int i = lane; i < p.max_parts; i += 32) m = fmaxf(m, ml[i].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));

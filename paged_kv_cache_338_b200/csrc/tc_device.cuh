@@ -168,7 +168,7 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo_bytes) {
 
 // Instruction descriptor of kind::f16: fp32 accumulator, A and B of one type
 // (f16 = 0, bf16 = 1), A K-major, B K-major or MN-major, M 128, N.
-__device__ __forceinline__ uint32_t idesc_f16(int ab_bf16, int b_mn_major, int N) {
+__host__ __device__ constexpr __forceinline__ uint32_t idesc_f16(int ab_bf16, int b_mn_major, int N) {
     return (1u << 4) | ((uint32_t)ab_bf16 << 7) | ((uint32_t)ab_bf16 << 10) |
            ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kMmaM >> 4) << 24);
 }
@@ -241,6 +241,55 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     ok = __all_sync(~0u, ok);
     if (!ok) *abort_flag = 1;
     return ok;
+}
+
+// Poll until the phase with the given parity completes, a few thousand times at
+// most (the loop of a wait that is about to be over: nothing else is in it).
+__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 4096;\n"
+        "SPIN_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE_%=;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra SPIN_%=;\n"
+        "DONE_%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// The rest of a long wait, at most 2 s.  Not inlined: a kernel has a dozen waits, and
+// code that hardly ever runs between the steps of its loops costs instruction fetches.
+static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                            unsigned int* err, unsigned site, bool honor_abort) {
+    const uint64_t t0 = global_ns();
+    bool ok = false;
+    while (!(ok = mbar_spin(bar, parity))) {
+        if (honor_abort && *abort_flag) break;
+        if (global_ns() - t0 > 2000000000ull) {
+            atomicOr(err, PA_DEV_WAIT_TIMEOUT | (site << 16));
+            break;
+        }
+    }
+    ok = __all_sync(~0u, ok);
+    if (!ok) *abort_flag = 1;
+    return ok;
+}
+
+// warp_wait with the long part out of line (the few-row kernel: 340 -> 239 us on 16
+// sequences of 2k-32k tokens, E4M3).  Not for a loop that keeps nearly every register
+// across its waits, since a call has to save them.
+__device__ __forceinline__ bool quick_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                           unsigned int* err, unsigned site,
+                                           bool honor_abort = true) {
+    if (__all_sync(~0u, mbar_spin(bar, parity))) return true;
+    return mbar_wait_long(bar, parity, abort_flag, err, site, honor_abort);
 }
 
 }  // namespace dev
