@@ -148,19 +148,32 @@ def pa_launch_count() -> int:
 
 
 _CUDA_AVAILABLE = None
+# the handle of a device's current stream without the Stream object around it
+# (0.3 us a call against 3-5 of torch.cuda.current_stream()), where torch has it
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _device() -> int:
+    """The current CUDA device, -1 without one (host-only calls: argument checks)."""
     global _CUDA_AVAILABLE
-    if stream is None:
+    if not _CUDA_AVAILABLE:
         if _CUDA_AVAILABLE is None:
             _CUDA_AVAILABLE = torch.cuda.is_available()
-        if not _CUDA_AVAILABLE:                 # host-only calls (argument checks)
-            return ctypes.c_void_p(0)
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if not _CUDA_AVAILABLE:
+            return -1
+        torch.cuda.init()
+    return torch._C._cuda_getDevice()
+
+
+def _stream(stream) -> int:
+    if stream is None:
+        dev = _device()
+        if dev < 0:
+            return 0
+        return _RAW_STREAM(dev) if _RAW_STREAM else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -202,21 +215,21 @@ def pa_reshape_and_cache(key: torch.Tensor, value: torch.Tensor, key_cache: torc
 def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
     """The work is enqueued on the current device's stream: every tensor must
     live there (a None is skipped)."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    dev = _device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
+        if t is not None and (t.get_device() != dev or dev < 0):
             raise PaError(1, f"tensors must be on the current CUDA device (got {t.device})")
 
 
 def _rows(t: torch.Tensor, shape, what: str) -> int:
     """The stride between tokens of a [T, H, D] tensor whose heads are packed."""
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise PaError(1, f"{what} must have shape {list(shape)}, got {list(t.shape)}")
     T, H, D = shape
-    s = t.stride()
-    if (s[2] != 1 and D > 1) or (s[1] != D and H > 1):
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and D > 1) or (s1 != D and H > 1):
         raise PaError(1, f"the heads of a token of {what} must be contiguous")
-    return s[0] if T > 1 else H * D
+    return s0 if T > 1 else H * D
 
 
 def pa_norm_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,

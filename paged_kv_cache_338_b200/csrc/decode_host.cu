@@ -135,6 +135,9 @@ int64_t parts_for(int max_ctx, int partition) {
     return ((int64_t)max_ctx + partition - 1) / partition;
 }
 
+// With a cap the decode kernels take scores as 2 log2 e / softcap times the product.
+constexpr double kDecodeCap = 2.0 * 1.4426950408889634;
+
 // Tokens a sequence's stages cover with a window: the window and the rest of
 // the stage (one block) its first token lies in.
 int scored_span(int max_ctx, int window, int bs) {
@@ -210,7 +213,8 @@ extern "C" pa_status pa_decode_suggest_partition(int S, int Hkv, int bs,
         return fail(PA_ERR_INVALID_ARG, "bad arguments");
     // Enough CTAs for several waves on 148 SMs (3 resident per SM) so the last
     // wave is short, with partitions as long as that allows (each CTA pays a
-    // start-up and drain of a few microseconds) and no shorter than 256 tokens.
+    // start-up and drain of a few microseconds) and no shorter than 256 tokens
+    // where the batch is not tiny.
     const int64_t want = 148LL * 3 * 4;
     int64_t maxn = 0;
     for (int s = 0; s < S; ++s) maxn = context_lens_host[s] > maxn ? context_lens_host[s] : maxn;
@@ -223,6 +227,9 @@ extern "C" pa_status pa_decode_suggest_partition(int S, int Hkv, int bs,
     int64_t best = 256;
     for (int64_t P = 256; P < maxn; P *= 2)
         if (items(P) >= want) best = P;
+    // A batch that leaves most SMs without a partition of 256 gets shorter ones (one
+    // sequence of 501 tokens, 8 kv heads, bf16: 256 tokens 22.7 us, 64 tokens 15.6).
+    while (best < maxn && best > 64 && items(best) < 148) best /= 2;
     best = (best + bs - 1) / bs * bs;
     *partition = best >= maxn ? 0 : (int)best;
     return PA_OK;
@@ -397,7 +404,7 @@ pa_status pa::decode_impl(void* out, const void* q, pa_dtype q_dt, const void* k
     p.qk_scale = (float)((double)scale * (double)k_scale * 1.4426950408889634);
     p.v_scale = v_scale;
     if (mod) {
-        chk = check_score_opts(*mod, scale, k_scale, 1.0, &p.qk_scale, &p.cap_log2);
+        chk = check_score_opts(*mod, scale, k_scale, kDecodeCap, &p.qk_scale, &p.cap_log2);
         if (chk) return chk;
         p.slopes = mod->slopes;
         p.window = mod->window;
@@ -508,7 +515,7 @@ extern "C" pa_status pa_decode_scored(void* out, const void* q, pa_dtype q_dt,
     o.window = window;
     o.key_start = key_start;
     float qk, cap;
-    const pa_status st = check_score_opts(o, scale, k_scale, 1.0, &qk, &cap);
+    const pa_status st = check_score_opts(o, scale, k_scale, kDecodeCap, &qk, &cap);
     if (st) return st;
     if (partition < 0)
         return fail(PA_ERR_INVALID_ARG, "partition must be >= 0 (no balanced grid)");

@@ -33,6 +33,7 @@ namespace {
 using namespace pa::dev;
 
 constexpr int kThreads = 128;
+constexpr int kWaves = 4;            // CTAs a resident slot takes, at most
 
 struct Params {
     uint8_t* q_out;
@@ -117,8 +118,18 @@ __device__ __forceinline__ uint2 to_e4m3x8(const float* f, float scale) {
     return make_uint2(w[0], w[1]);
 }
 
-// One warp: passes [p0, p1) of token t.  A pass is ROWS head rows of one kind:
-// the query heads first, then the key heads, then the value heads.
+// The norm weights of a lane's two chunks, as they are stored.
+template <int IN> struct Weights {
+    Raw8<IN> a, b;
+    __device__ __forceinline__ void load(const uint8_t* w, int ea, int eb) {
+        a.load(w, ea);
+        b.load(w, eb);
+    }
+};
+
+// One warp: passes [p0, p1) of a token, then of the token `stride` units on.  A
+// pass is ROWS head rows of one kind: the query heads first, then the key heads,
+// then the value heads.
 template <int IN, bool TO_FP8, int D>
 __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const Params p) {
     constexpr int LANES = D / 16;                 // lanes of a row
@@ -129,122 +140,130 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const Params
     grid_dependency_wait();        // launched as a dependent of the kernel before it
     launch_dependents();
     const int lane = threadIdx.x & 31, sub = lane % LANES, row = lane / LANES;
-    const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const long long t = unit / p.split;
-    if (t >= p.T) return;
+    const long long units = (long long)p.T * p.split;
+    const long long stride = (long long)gridDim.x * (kThreads / 32);
     const int nq = (p.Hq + ROWS - 1) / ROWS, nkv = (p.Hkv + ROWS - 1) / ROWS;
     const int passes = nq + 2 * nkv;
-    const int part = (int)(unit % p.split);
-    const int p0 = (int)((long long)passes * part / p.split);
-    const int p1 = (int)((long long)passes * (part + 1) / p.split);
 
     // this lane's two chunks of a row, in elements
     const int half = p.rot_dim / 16;              // lanes that rotate
     const bool turns = sub < half;
     const int ea = turns ? 8 * sub : p.rot_dim + 16 * (sub - half);
     const int eb = turns ? p.rot_dim / 2 + 8 * sub : ea + 8;
+    // first cosine of the lane's pairs 0-3 and 4-7: pairs (e, e + rot/2) have index
+    // e, adjacent pairs (2j, 2j + 1) index j
+    const int j0 = p.interleaved ? ea / 2 : ea, j1 = p.interleaved ? eb / 2 : ea + 4;
+    Weights<IN> wq, wk;
+    if (p.q_weight) wq.load(p.q_weight, ea, eb);
+    if (p.k_weight) wk.load(p.k_weight, ea, eb);
 
-    const int64_t slot = p.slots[t];
-    const bool write = slot >= 0 && slot < p.nslots;
-    if (slot >= p.nslots && lane == 0) raise_error(p.err, PA_DEV_BAD_SLOT);
-    float cs[8], sn[8];                           // of pairs 0..7 of this lane
-    if (half > 0) {
-        const int64_t pos = p.positions[t];
-        if (pos < 0 || pos >= p.table_rows) {     // warp-uniform: the token is skipped
+    for (long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); unit < units;
+         unit += stride) {
+        const long long t = unit / p.split;
+        const int part = (int)(unit % p.split);
+        const int p0 = (int)((long long)passes * part / p.split);
+        const int p1 = (int)((long long)passes * (part + 1) / p.split);
+        const int64_t slot = p.slots[t];
+        const int64_t pos = half > 0 ? p.positions[t] : 0;
+        const bool write = slot >= 0 && slot < p.nslots;
+        if (slot >= p.nslots && lane == 0) raise_error(p.err, PA_DEV_BAD_SLOT);
+        if (half > 0 && (pos < 0 || pos >= p.table_rows)) {   // warp-uniform: the token is skipped
             if (lane == 0) raise_error(p.err, PA_DEV_BAD_POSITION);
-            return;
+            continue;
         }
+        float4 c0 = {}, c1 = {}, s0 = {}, s1 = {};
         if (turns) {
-            // pairs (e, e + rot/2): pair index e; adjacent pairs (2j, 2j + 1): j
             const float* tr = p.cos_sin + pos * p.rot_dim;
-            const int j0 = p.interleaved ? ea / 2 : ea, j1 = p.interleaved ? eb / 2 : ea + 4;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                cs[i] = tr[j0 + i];
-                cs[4 + i] = tr[j1 + i];
-                sn[i] = tr[p.rot_dim / 2 + j0 + i];
-                sn[4 + i] = tr[p.rot_dim / 2 + j1 + i];
-            }
+            c0 = *reinterpret_cast<const float4*>(tr + j0);
+            c1 = *reinterpret_cast<const float4*>(tr + j1);
+            s0 = *reinterpret_cast<const float4*>(tr + p.rot_dim / 2 + j0);
+            s1 = *reinterpret_cast<const float4*>(tr + p.rot_dim / 2 + j1);
         }
-    }
+        const float cs[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        const float sn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 
-    for (int pb = p0; pb < p1; pb += kPasses) {
-        Raw8<IN> ra[kPasses], rb[kPasses];
-        auto place = [&](int ps, int& kind, int& h, int& heads) {
-            kind = ps < nq ? 0 : ps < nq + nkv ? 1 : 2;
-            h = (ps - (kind == 0 ? 0 : kind == 1 ? nq : nq + nkv)) * ROWS + row;
-            heads = kind == 0 ? p.Hq : p.Hkv;
-        };
+        for (int pb = p0; pb < p1; pb += kPasses) {
+            Raw8<IN> ra[kPasses], rb[kPasses];
+            auto place = [&](int ps, int& kind, int& h) {
+                kind = ps < nq ? 0 : ps < nq + nkv ? 1 : 2;
+                h = (ps - (kind == 0 ? 0 : kind == 1 ? nq : nq + nkv)) * ROWS + row;
+                return ps < p1 && h < (kind == 0 ? p.Hq : p.Hkv) && (kind == 0 || write);
+            };
 #pragma unroll
-        for (int u = 0; u < kPasses; ++u) {
-            int kind, h, heads;
-            place(pb + u, kind, h, heads);
-            if (pb + u < p1 && h < heads && (kind == 0 || write)) {
-                const uint8_t* src = kind == 0   ? p.q + t * p.q_stride
-                                     : kind == 1 ? p.k + t * p.k_stride
-                                                 : p.v + t * p.v_stride;
-                ra[u].load(src + (size_t)h * D * E, ea);
-                rb[u].load(src + (size_t)h * D * E, eb);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kPasses; ++u) {
-            int kind, h, heads;
-            place(pb + u, kind, h, heads);
-            const bool live = pb + u < p1 && h < heads && (kind == 0 || write);
-            float y[16];
-            ra[u].to_float(y);
-            rb[u].to_float(y + 8);
-            const uint8_t* wt = kind == 0 ? p.q_weight : p.k_weight;
-            if (kind < 2 && wt) {                 // warp-uniform
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
-#pragma unroll
-                for (int x = LANES / 2; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
-                const float inv = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-                Raw8<IN> wr;
-                float w[16];
-                wr.load(wt, ea);
-                wr.to_float(w);
-                wr.load(wt, eb);
-                wr.to_float(w + 8);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = y[i] * inv * (w[i] + p.weight_offset);
-            }
-            if (kind < 2 && turns) {
-                if (p.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float a = y[2 * i], b = y[2 * i + 1];
-                        y[2 * i] = a * cs[i] - b * sn[i];
-                        y[2 * i + 1] = b * cs[i] + a * sn[i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float a = y[i], b = y[8 + i];
-                        y[i] = a * cs[i] - b * sn[i];
-                        y[8 + i] = b * cs[i] + a * sn[i];
-                    }
+            for (int u = 0; u < kPasses; ++u) {
+                int kind, h;
+                if (place(pb + u, kind, h)) {
+                    const uint8_t* src = (kind == 0   ? p.q + t * p.q_stride
+                                          : kind == 1 ? p.k + t * p.k_stride
+                                                      : p.v + t * p.v_stride) + (size_t)h * D * E;
+                    ra[u].load(src, ea);
+                    rb[u].load(src, eb);
                 }
             }
-            if (!live) continue;
-            if (kind == 0 || !TO_FP8) {
-                uint8_t* dst = kind == 0 ? p.q_out + t * p.q_out_stride + (size_t)h * D * E
-                                         : (kind == 1 ? p.kc : p.vc) +
-                                               ((size_t)slot * p.Hkv + h) * D * EC;
-                if (kind < 2) {                   // a value row is copied as it was read
+#pragma unroll
+            for (int u = 0; u < kPasses; ++u) {
+                int kind, h;
+                const bool live = place(pb + u, kind, h);
+                if (pb + u >= p1) break;                      // warp-uniform
+                if (kind == 2 && !TO_FP8) {                   // a value row goes as it came
+                    if (live) {
+                        uint8_t* dst = p.vc + ((size_t)slot * p.Hkv + h) * D * EC;
+                        ra[u].store(dst, ea);
+                        rb[u].store(dst, eb);
+                    }
+                    continue;
+                }
+                float y[16];
+                ra[u].to_float(y);
+                rb[u].to_float(y + 8);
+                if (kind < 2) {
+                    if (kind == 0 ? p.q_weight : p.k_weight) {
+                        float ss[4] = {};
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) ss[i & 3] = fmaf(y[i], y[i], ss[i & 3]);
+                        float sum = (ss[0] + ss[1]) + (ss[2] + ss[3]);
+#pragma unroll
+                        for (int x = LANES / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                        const float inv = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+                        const Weights<IN>& wr = kind == 0 ? wq : wk;
+                        float w[16];
+                        wr.a.to_float(w);
+                        wr.b.to_float(w + 8);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[i] = y[i] * inv * (w[i] + p.weight_offset);
+                    }
+                    if (turns) {
+                        if (p.interleaved) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float a = y[2 * i], b = y[2 * i + 1];
+                                y[2 * i] = a * cs[i] - b * sn[i];
+                                y[2 * i + 1] = b * cs[i] + a * sn[i];
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float a = y[i], b = y[8 + i];
+                                y[i] = a * cs[i] - b * sn[i];
+                                y[8 + i] = b * cs[i] + a * sn[i];
+                            }
+                        }
+                    }
+                }
+                if (!live) continue;
+                if (kind == 0 || !TO_FP8) {
+                    uint8_t* dst = kind == 0 ? p.q_out + t * p.q_out_stride + (size_t)h * D * E
+                                             : p.kc + ((size_t)slot * p.Hkv + h) * D * EC;
                     ra[u].from_float(y);
                     rb[u].from_float(y + 8);
+                    ra[u].store(dst, ea);
+                    rb[u].store(dst, eb);
+                } else {
+                    uint8_t* dst = (kind == 1 ? p.kc : p.vc) + ((size_t)slot * p.Hkv + h) * D;
+                    const float sc = kind == 1 ? p.k_scale : p.v_scale;
+                    *reinterpret_cast<uint2*>(dst + ea) = to_e4m3x8(y, sc);
+                    *reinterpret_cast<uint2*>(dst + eb) = to_e4m3x8(y + 8, sc);
                 }
-                ra[u].store(dst, ea);
-                rb[u].store(dst, eb);
-            } else {
-                uint8_t* dst = (kind == 1 ? p.kc : p.vc) + ((size_t)slot * p.Hkv + h) * D;
-                const float sc = kind == 1 ? p.k_scale : p.v_scale;
-                *reinterpret_cast<uint2*>(dst + ea) = to_e4m3x8(y, sc);
-                *reinterpret_cast<uint2*>(dst + eb) = to_e4m3x8(y + 8, sc);
             }
         }
     }
@@ -253,15 +272,20 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const Params
 template <int IN, bool TO_FP8, int D>
 cudaError_t launch(Params p, cudaStream_t st) {
     constexpr int ROWS = 32 * 16 / D;
+    constexpr long long per = kThreads / 32;
     const int passes = (p.Hq + ROWS - 1) / ROWS + 2 * ((p.Hkv + ROWS - 1) / ROWS);
-    // Enough warps to fill the GPU (16 per SM) where the tokens alone do not:
-    // down to one pass a warp.
+    // Enough warps to fill the GPU (16 per SM) where the tokens alone do not: down
+    // to one pass a warp.  Where there are more, a warp takes several tokens and
+    // keeps the weights.
     const long long want = 148LL * 16;
     long long split = (want + p.T - 1) / p.T;
     p.split = (int)(split < passes ? split : passes);
-    const long long units = (long long)p.T * p.split;
-    const long long per = kThreads / 32;
-    return launch_pdl(norm_rope_append_kernel<IN, TO_FP8, D>, dim3((unsigned)((units + per - 1) / per)),
+    const long long blocks = ((long long)p.T * p.split + per - 1) / per;
+    int resident = 0;
+    const cudaError_t e = occupancy<norm_rope_append_kernel<IN, TO_FP8, D>>(&resident, kThreads, 0);
+    if (e != cudaSuccess) return e;
+    const long long most = 148LL * (resident > 0 ? resident : 1) * kWaves;
+    return launch_pdl(norm_rope_append_kernel<IN, TO_FP8, D>, dim3((unsigned)(blocks < most ? blocks : most)),
                       dim3(kThreads), 0, st, p);
 }
 

@@ -100,6 +100,15 @@ def test_workspace_sizes():
     assert g(3, 8, 128, 16, 1000, 100, 64) == pa.pa_decode_workspace_size(3, 8, 128, 115, 64)
 
 
+def test_tiny_batches_split_further():
+    f = pa.pa_decode_suggest_partition
+    assert f(8, 16, [501]) == 64
+    assert f(8, 16, [4000]) == 128                            # 16 x 8 partitions of 256: 128 < 148
+    assert f(8, 16, [2000] * 3) == 256                        # 3 x 8 x 8 = 192
+    assert f(8, 16, [200]) == 0 and f(8, 16, [256]) == 0      # short ones stay in one pass
+    assert f(8, 16, [501] * 64) == 256 and f(32, 16, [64] * 4096) == 0
+
+
 def test_suggested_parts():
     f = pa.pa_prefill_scored_suggest_partition
     for S in (1, 3, 16, 200):
