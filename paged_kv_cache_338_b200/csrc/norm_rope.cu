@@ -19,21 +19,27 @@
 // loads in flight before the first use.
 //
 // The work is one read of q, k, v and one write of each: HBM-bound for many
-// tokens, latency-bound for a decode step, where the passes of a token are
-// spread over `split` warps (see pa_norm_rope_append).
+// tokens (32768 of 32/8 heads of 128, bf16: 149 us, 5.5 TB/s; into E4M3 152 us),
+// latency-bound for a decode step (8 tokens: 3.1 us), where the passes of a token
+// are spread over `split` warps.  Rows are worked on two elements an instruction:
+// with one the issue slots were half taken and the registers held 12 warps an SM.
 #include <cuda_runtime.h>
 
 #include <cmath>
 
-#include "pa_device.cuh"
 #include "pa_internal.h"
+#include "tc_device.cuh"
 
 namespace {
 
 using namespace pa::dev;
 
 constexpr int kThreads = 128;
-constexpr int kWaves = 4;            // CTAs a resident slot takes, at most
+// Passes whose loads are in flight, and CTAs an SM holds at least (which bounds the
+// registers).  32768 tokens, 32/8 heads of 128, bf16: 2 passes and 4 CTAs 150 us, 2 and
+// 5 166 (spills), 4 and 3 170, 1 and 6 186.
+constexpr int kPasses = 2;
+constexpr int kBlocks = 4;
 
 struct Params {
     uint8_t* q_out;
@@ -48,7 +54,7 @@ struct Params {
     uint8_t *kc, *vc;
     const int64_t* slots;
     long long nslots;
-    float k_scale, v_scale;
+    float k_scale, v_scale, k_inverse, v_inverse;
     unsigned int* err;
     int T, Hq, Hkv;
     int split;                                               // warps per token
@@ -102,44 +108,144 @@ template <int DT> struct Raw16 {
 template <> struct Raw8<PA_F16> : Raw16<PA_F16> {};
 template <> struct Raw8<PA_BF16> : Raw16<PA_BF16> {};
 
-// 8 floats to 8 E4M3 codes of x / scale (binary32 division, to nearest even,
-// saturating), the cache append's rounding.
-__device__ __forceinline__ uint2 to_e4m3x8(const float* f, float scale) {
+// x / scale in binary32, to nearest even, as the cache append divides.  With
+// `inverse` = 1 / scale rounded to nearest (0: a scale outside 2^-60..2^60) one
+// residual step gives the correctly rounded quotient (Markstein's theorem).  Past 512
+// a quotient saturates whatever its last bits, and below 2^-12 it is a zero code of
+// its sign (which the step would lose), so both ends go without.
+__device__ __forceinline__ float quotient(float x, float scale, float inverse) {
+    const float q = x * inverse;
+    const float r = fmaf(fmaf(-q, scale, x), inverse, q);
+    return fabsf(q) < 512.f && fabsf(q) > 0x1p-12f ? r : q;
+}
+
+// 8 floats to 8 E4M3 codes of x / scale, to nearest even, saturating.
+__device__ __forceinline__ uint2 to_e4m3x8(const float* f, float scale, float inverse) {
     uint32_t w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         w[k] = 0;
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
-            const float2 y = make_float2(__fdiv_rn(f[4 * k + j], scale), __fdiv_rn(f[4 * k + j + 1], scale));
+            const float a = f[4 * k + j], b = f[4 * k + j + 1];
+            const float2 y = inverse != 0.f
+                                 ? make_float2(quotient(a, scale, inverse), quotient(b, scale, inverse))
+                                 : make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale));
             w[k] |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (8 * j);
         }
     }
     return make_uint2(w[0], w[1]);
 }
 
-// The norm weights of a lane's two chunks, as they are stored.
-template <int IN> struct Weights {
-    Raw8<IN> a, b;
-    __device__ __forceinline__ void load(const uint8_t* w, int ea, int eb) {
-        a.load(w, ea);
-        b.load(w, eb);
-    }
-};
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 
-// One warp: passes [p0, p1) of a token, then of the token `stride` units on.  A
-// pass is ROWS head rows of one kind: the query heads first, then the key heads,
-// then the value heads.
+// The passes [lo, hi) of one kind of a token (KIND 0 queries, 1 keys, 2 values):
+// kPasses batches of loads before the first use.  A pass is ROWS heads.
+template <int IN, bool TO_FP8, int D, int KIND>
+__device__ __forceinline__ void token_passes(const Params& p, const uint8_t* src, uint8_t* dst, int lo,
+                                             int hi, int ea, int eb, bool turns, const float* cs,
+                                             const float* sn, const float2* w, bool norm) {
+    constexpr int LANES = D / 16, ROWS = 32 / LANES;
+    constexpr int E = Storage<IN>::bytes;
+    constexpr bool CODES = TO_FP8 && KIND > 0;     // E4M3 out
+    constexpr int EO = CODES ? 1 : E;
+    const int heads = KIND == 0 ? p.Hq : p.Hkv;
+    const int row = (threadIdx.x & 31) / LANES;
+#pragma unroll 1
+    for (int pb = lo; pb < hi; pb += kPasses) {
+        Raw8<IN> ra[kPasses], rb[kPasses];
+#pragma unroll
+        for (int u = 0; u < kPasses; ++u) {
+            const int h = (pb + u) * ROWS + row;
+            if (pb + u < hi && h < heads) {
+                ra[u].load(src + (size_t)h * D * E, ea);
+                rb[u].load(src + (size_t)h * D * E, eb);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kPasses; ++u) {
+            if (pb + u >= hi) break;               // warp-uniform
+            const int h = (pb + u) * ROWS + row;
+            uint8_t* out = dst + (size_t)h * D * EO;
+            if constexpr (KIND == 2 && !TO_FP8) {  // a value row goes as it came
+                if (h < heads) {
+                    ra[u].store(out, ea);
+                    rb[u].store(out, eb);
+                }
+            } else {
+                float f[16];
+                ra[u].to_float(f);
+                rb[u].to_float(f + 8);
+                if constexpr (KIND < 2) {
+                    float2 y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = make_float2(f[2 * i], f[2 * i + 1]);
+                    if (norm) {                    // warp-uniform
+                        float2 ss[2] = {};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) ss[i & 1] = fma2(y[i], y[i], ss[i & 1]);
+                        float sum = (ss[0].x + ss[0].y) + (ss[1].x + ss[1].y);
+#pragma unroll
+                        for (int x = LANES / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                        const float inv = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = mul2(mul2(y[i], make_float2(inv, inv)), w[i]);
+                    }
+                    if (turns) {
+                        if (p.interleaved) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float a = y[i].x, b = y[i].y;
+                                y[i] = make_float2(a * cs[i] - b * sn[i], b * cs[i] + a * sn[i]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 c = make_float2(cs[2 * i], cs[2 * i + 1]);
+                                const float2 s = make_float2(sn[2 * i], sn[2 * i + 1]);
+                                const float2 a = y[i], b = y[4 + i];
+                                y[i] = fma2(a, c, mul2(b, make_float2(-s.x, -s.y)));
+                                y[4 + i] = fma2(b, c, mul2(a, s));
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[2 * i] = y[i].x, f[2 * i + 1] = y[i].y;
+                }
+                if (h >= heads) continue;
+                if constexpr (CODES) {
+                    const float sc = KIND == 1 ? p.k_scale : p.v_scale;
+                    const float inv = KIND == 1 ? p.k_inverse : p.v_inverse;
+                    *reinterpret_cast<uint2*>(out + ea) = to_e4m3x8(f, sc, inv);
+                    *reinterpret_cast<uint2*>(out + eb) = to_e4m3x8(f + 8, sc, inv);
+                } else {
+                    ra[u].from_float(f);
+                    rb[u].from_float(f + 8);
+                    ra[u].store(out, ea);
+                    rb[u].store(out, eb);
+                }
+            }
+        }
+    }
+}
+
+// One warp: its share of the passes of a token (the query heads' first, then the
+// key heads', then the value heads'), then of the token `stride` units on.
 template <int IN, bool TO_FP8, int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, IN == PA_F32 ? 3 : kBlocks) norm_rope_append_kernel(const Params p) {
     constexpr int LANES = D / 16;                 // lanes of a row
     constexpr int ROWS = 32 / LANES;              // rows of a pass
-    constexpr int E = Storage<IN>::bytes;
-    constexpr int EC = TO_FP8 ? 1 : E;
-    constexpr int kPasses = IN == PA_F32 ? 2 : 4; // passes of loads in flight
+    constexpr int EC = TO_FP8 ? 1 : Storage<IN>::bytes;
     grid_dependency_wait();        // launched as a dependent of the kernel before it
     launch_dependents();
-    const int lane = threadIdx.x & 31, sub = lane % LANES, row = lane / LANES;
+    const int lane = threadIdx.x & 31, sub = lane % LANES;
     const long long units = (long long)p.T * p.split;
     const long long stride = (long long)gridDim.x * (kThreads / 32);
     const int nq = (p.Hq + ROWS - 1) / ROWS, nkv = (p.Hkv + ROWS - 1) / ROWS;
@@ -153,9 +259,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const Params
     // first cosine of the lane's pairs 0-3 and 4-7: pairs (e, e + rot/2) have index
     // e, adjacent pairs (2j, 2j + 1) index j
     const int j0 = p.interleaved ? ea / 2 : ea, j1 = p.interleaved ? eb / 2 : ea + 4;
-    Weights<IN> wq, wk;
-    if (p.q_weight) wq.load(p.q_weight, ea, eb);
-    if (p.k_weight) wk.load(p.k_weight, ea, eb);
 
     for (long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); unit < units;
          unit += stride) {
@@ -181,91 +284,33 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const Params
         }
         const float cs[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
         const float sn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-
-        for (int pb = p0; pb < p1; pb += kPasses) {
-            Raw8<IN> ra[kPasses], rb[kPasses];
-            auto place = [&](int ps, int& kind, int& h) {
-                kind = ps < nq ? 0 : ps < nq + nkv ? 1 : 2;
-                h = (ps - (kind == 0 ? 0 : kind == 1 ? nq : nq + nkv)) * ROWS + row;
-                return ps < p1 && h < (kind == 0 ? p.Hq : p.Hkv) && (kind == 0 || write);
-            };
+        float2 w[8];
+        auto weights = [&](const uint8_t* src) {
+            if (!src) return false;
+            Raw8<IN> a, b;
+            float f[16];
+            a.load(src, ea);
+            b.load(src, eb);
+            a.to_float(f);
+            b.to_float(f + 8);
 #pragma unroll
-            for (int u = 0; u < kPasses; ++u) {
-                int kind, h;
-                if (place(pb + u, kind, h)) {
-                    const uint8_t* src = (kind == 0   ? p.q + t * p.q_stride
-                                          : kind == 1 ? p.k + t * p.k_stride
-                                                      : p.v + t * p.v_stride) + (size_t)h * D * E;
-                    ra[u].load(src, ea);
-                    rb[u].load(src, eb);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kPasses; ++u) {
-                int kind, h;
-                const bool live = place(pb + u, kind, h);
-                if (pb + u >= p1) break;                      // warp-uniform
-                if (kind == 2 && !TO_FP8) {                   // a value row goes as it came
-                    if (live) {
-                        uint8_t* dst = p.vc + ((size_t)slot * p.Hkv + h) * D * EC;
-                        ra[u].store(dst, ea);
-                        rb[u].store(dst, eb);
-                    }
-                    continue;
-                }
-                float y[16];
-                ra[u].to_float(y);
-                rb[u].to_float(y + 8);
-                if (kind < 2) {
-                    if (kind == 0 ? p.q_weight : p.k_weight) {
-                        float ss[4] = {};
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) ss[i & 3] = fmaf(y[i], y[i], ss[i & 3]);
-                        float sum = (ss[0] + ss[1]) + (ss[2] + ss[3]);
-#pragma unroll
-                        for (int x = LANES / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-                        const float inv = rsqrtf(fmaf(sum, 1.f / D, p.eps));
-                        const Weights<IN>& wr = kind == 0 ? wq : wk;
-                        float w[16];
-                        wr.a.to_float(w);
-                        wr.b.to_float(w + 8);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = y[i] * inv * (w[i] + p.weight_offset);
-                    }
-                    if (turns) {
-                        if (p.interleaved) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float a = y[2 * i], b = y[2 * i + 1];
-                                y[2 * i] = a * cs[i] - b * sn[i];
-                                y[2 * i + 1] = b * cs[i] + a * sn[i];
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float a = y[i], b = y[8 + i];
-                                y[i] = a * cs[i] - b * sn[i];
-                                y[8 + i] = b * cs[i] + a * sn[i];
-                            }
-                        }
-                    }
-                }
-                if (!live) continue;
-                if (kind == 0 || !TO_FP8) {
-                    uint8_t* dst = kind == 0 ? p.q_out + t * p.q_out_stride + (size_t)h * D * E
-                                             : p.kc + ((size_t)slot * p.Hkv + h) * D * EC;
-                    ra[u].from_float(y);
-                    rb[u].from_float(y + 8);
-                    ra[u].store(dst, ea);
-                    rb[u].store(dst, eb);
-                } else {
-                    uint8_t* dst = (kind == 1 ? p.kc : p.vc) + ((size_t)slot * p.Hkv + h) * D;
-                    const float sc = kind == 1 ? p.k_scale : p.v_scale;
-                    *reinterpret_cast<uint2*>(dst + ea) = to_e4m3x8(y, sc);
-                    *reinterpret_cast<uint2*>(dst + eb) = to_e4m3x8(y + 8, sc);
-                }
-            }
+            for (int i = 0; i < 8; ++i) w[i] = make_float2(f[2 * i] + p.weight_offset, f[2 * i + 1] + p.weight_offset);
+            return true;
+        };
+        const size_t cache = write ? (size_t)slot * p.Hkv * D * EC : 0;
+        if (p0 < nq) {
+            const bool norm = weights(p.q_weight);
+            token_passes<IN, TO_FP8, D, 0>(p, p.q + t * p.q_stride, p.q_out + t * p.q_out_stride, p0,
+                                           min(p1, nq), ea, eb, turns, cs, sn, w, norm);
         }
+        if (write && p1 > nq && p0 < nq + nkv) {
+            const bool norm = weights(p.k_weight);
+            token_passes<IN, TO_FP8, D, 1>(p, p.k + t * p.k_stride, p.kc + cache, max(p0 - nq, 0),
+                                           min(p1 - nq, nkv), ea, eb, turns, cs, sn, w, norm);
+        }
+        if (write && p1 > nq + nkv)
+            token_passes<IN, TO_FP8, D, 2>(p, p.v + t * p.v_stride, p.vc + cache, max(p0 - nq - nkv, 0),
+                                           p1 - nq - nkv, ea, eb, turns, cs, sn, w, false);
     }
 }
 
@@ -275,8 +320,9 @@ cudaError_t launch(Params p, cudaStream_t st) {
     constexpr long long per = kThreads / 32;
     const int passes = (p.Hq + ROWS - 1) / ROWS + 2 * ((p.Hkv + ROWS - 1) / ROWS);
     // Enough warps to fill the GPU (16 per SM) where the tokens alone do not: down
-    // to one pass a warp.  Where there are more, a warp takes several tokens and
-    // keeps the weights.
+    // to one pass a warp.  Where there are more than the GPU holds at once, a warp
+    // takes several tokens (32768 tokens: 149 us, with four times the CTAs 150, with
+    // sixteen times 156).
     const long long want = 148LL * 16;
     long long split = (want + p.T - 1) / p.T;
     p.split = (int)(split < passes ? split : passes);
@@ -284,7 +330,7 @@ cudaError_t launch(Params p, cudaStream_t st) {
     int resident = 0;
     const cudaError_t e = occupancy<norm_rope_append_kernel<IN, TO_FP8, D>>(&resident, kThreads, 0);
     if (e != cudaSuccess) return e;
-    const long long most = 148LL * (resident > 0 ? resident : 1) * kWaves;
+    const long long most = 148LL * (resident > 0 ? resident : 1);
     return launch_pdl(norm_rope_append_kernel<IN, TO_FP8, D>, dim3((unsigned)(blocks < most ? blocks : most)),
                       dim3(kThreads), 0, st, p);
 }
@@ -297,6 +343,11 @@ cudaError_t launch_dim(const Params& p, int D, cudaStream_t st) {
     case 256: return launch<IN, TO_FP8, 256>(p, st);
     }
     return cudaErrorNotSupported;
+}
+
+// 1 / scale to nearest, 0 where a quotient by it may leave the normal range.
+float inverse_of(float scale) {
+    return scale >= 0x1p-60f && scale <= 0x1p60f ? 1.f / scale : 0.f;
 }
 
 }  // namespace
@@ -378,6 +429,8 @@ extern "C" pa_status pa_norm_rope_append(
     p.nslots = NB * bs;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
+    p.k_inverse = inverse_of(k_scale);
+    p.v_inverse = inverse_of(v_scale);
     p.err = err;
     p.T = T;
     p.Hq = Hq;

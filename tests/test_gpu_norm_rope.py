@@ -158,6 +158,30 @@ def test_without_norm_and_rotation_it_is_the_plain_append():
         assert torch.equal(vc.view(torch.uint8), v2.cpu().view(torch.uint8))
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.02, 3.3e-3, 0.1, 7.0, 1e-17, 3e17, 1e-30, 7e25])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_codes_are_the_plain_append_s_for_any_value_and_scale(dt, scale):
+    """Values of every exponent, borders between codes and their neighbours: bit for bit."""
+    g = torch.Generator().manual_seed(11)
+    T, Hkv, D = 512, 4, 128
+    n = T * Hkv * D
+    codes = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float().nan_to_num(448.0)
+    mid = (codes[torch.randint(0, 256, (n // 4,), generator=g)] * (1 + torch.randint(-3, 4, (n // 4,), generator=g) * 2.0 ** -5)).double() * scale
+    wide = torch.randn(n // 4, generator=g).double() * 2.0 ** torch.randint(-140, 120, (n // 4,), generator=g).double()
+    near = torch.randn(n // 2, generator=g).double() * 150 * scale
+    x = torch.cat([mid, wide, near]).clamp(-3e38, 3e38).float()
+    x[:6] = torch.tensor([0.0, -0.0, float("inf"), -float("inf"), float("nan"), 448.0 * scale])
+    x = x[torch.randperm(n, generator=g)].view(T, Hkv, D).to(DT[dt]).cuda()
+    caches = [torch.zeros(T // 16, 16, Hkv, D, device="cuda", dtype=torch.uint8).view(DT["fp8"]) for _ in range(4)]
+    slots = torch.arange(T, device="cuda")
+    q = torch.zeros(T, 4, D, dtype=x.dtype, device="cuda")
+    pa.pa_norm_rope_append(q, q, x, x.flip(0).contiguous(), None, None, 0.0, None, None, caches[0], caches[1],
+                           slots, k_scale=scale, v_scale=scale * 0.75)
+    pa.pa_reshape_and_cache(x, x.flip(0).contiguous(), caches[2], caches[3], slots, scale, scale * 0.75)
+    for a, b in zip(caches[:2], caches[2:]):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 def test_bad_slots_and_positions_are_reported_not_followed():
     c = _case(30, 8, 2, 128, 16, "bf16", "bf16", True, 128, False, seed=6)
     c["slots"][:] = torch.randperm(c["kc"].shape[0] * 16, generator=torch.Generator().manual_seed(1))[:30]
