@@ -36,8 +36,13 @@ template <bool FP8, int D, int NR>
 struct FewPlan {
     static constexpr int NSEG = D / 64;
     static constexpr int TILE = NSEG * kSeg;
-    // 16-bit: ring of K and V tiles in turn; 8-bit: two V operand tiles, ring of codes
-    static constexpr int NS = FP8 ? 2 : D == 64 ? 10 : 5;
+    // Operand slots: 16-bit a ring of KS K tiles and one of VS V tiles, 8-bit V tiles
+    // and a ring of codes.  Every slot has one warp that waits for it: a wait goes by
+    // the parity of the slot's phase, which a warp that skips a phase of it can mistake
+    // for the one before (K and V in one ring of five did, and released slots under
+    // copies in flight).
+    static constexpr int KS = FP8 ? 0 : D == 64 ? 5 : 3, VS = FP8 ? 2 : D == 64 ? 5 : 2;
+    static constexpr int NS = KS + VS;
     static constexpr int RS = FP8 ? 6 : 0;
     static constexpr int NG = NR / 16;                  // softmax warpgroups, 16 rows each
     static constexpr int QB = NR * 128 * NSEG;
@@ -76,7 +81,7 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                    const __grid_constant__ CUtensorMap tmv, const Params p) {
     using L = FewPlan<FP8, D, NR>;
     constexpr int OT = FP8 ? (int)PA_F16 : QT;
-    constexpr int NSEG = L::NSEG, NS = L::NS, RS = L::RS;
+    constexpr int NSEG = L::NSEG, NS = L::NS, RS = L::RS, KS = L::KS, VS = L::VS;
     constexpr bool QCONV = FP8 && QT == PA_BF16;
     constexpr float SHIFT = OT == PA_F16 ? 7.f : 0.f;      // as in the kernel for many rows
     grid_dependency_wait();
@@ -228,7 +233,6 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             for (int sg = 0; sg < NSEG; ++sg)
                 tma_load_3d(sb + L::Q + sg * NR * 128, &tmq, q_full, sg * 64, g * p.G, q0);
         }
-        constexpr int RING = FP8 ? RS : NS;
         constexpr uint32_t TX = FP8 ? kSeg : L::TILE;
         // 32 table entries a time, the next ones on the way; a block past the last
         // visible key, or an id outside the cache, reads block NB: zeros
@@ -236,9 +240,14 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             const int lb = ((kb + t * kBN) >> p.log2bs) + lane;
             return ((long long)lb << p.log2bs) <= hi_c ? p.block_tables[(size_t)s * p.MB + lb] : INT_MIN;
         };
-        int started = 0, next = entry(0), ids = 0;
+        // K_j and V_j: the use and the slot of the ring (8-bit: uses 2j, 2j + 1 of one ring)
+        auto use = [&](int j, int kv) { return FP8 ? 2 * j + kv : j; };
+        auto ring = [&](int kv) { return FP8 ? RS : kv ? VS : KS; };
+        auto filled = [&](int kv, int st) { return FP8 ? raw_full(st) : full(kv ? KS + st : st); };
+        int started[2] = {0, 0}, next = entry(0), ids = 0;
+        bool ok = true;
 #pragma unroll 1
-        for (int j = 0; j < nt; ++j) {
+        for (int j = 0; j < nt && ok; ++j) {
             if (j % tpf == 0) {
                 const int e = next;
                 const bool in = e >= 0 && (long long)e < p.NB;
@@ -248,13 +257,12 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                 next = entry(j + tpf);
             }
             const int id = __shfl_sync(~0u, ids, ((j % tpf) * bpt + lane) & 31);
-            bool ok = true;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
-                const int u = 2 * j + kv, st = u % RING;
-                const uint32_t fb = FP8 ? raw_full(st) : full(st);
-                ok = quick_wait(FP8 ? raw_free(st) : free_(st), ((u / RING) & 1) ^ 1, abort_flag, p.err,
-                               10 + kv);
+                const int u = use(j, kv), st = u % ring(kv), slot = FP8 ? st : kv ? KS + st : st;
+                const uint32_t fb = filled(kv, st);
+                ok = ok && quick_wait(FP8 ? raw_free(st) : free_(slot), ((u / ring(kv)) & 1) ^ 1, abort_flag,
+                                      p.err, 10 + kv);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(fb, TX);
                 __syncwarp();
@@ -265,19 +273,22 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                     } else {
 #pragma unroll 1
                         for (int sg = 0; sg < NSEG; ++sg)
-                            tma_load_4d_plain(sb + L::OP + st * L::TILE + sg * kSeg + lane * box,
+                            tma_load_4d_plain(sb + L::OP + slot * L::TILE + sg * kSeg + lane * box,
                                               kv ? &tmv : &tmk, fb, sg * 64, g, 0, id);
                     }
                 }
-                started = u + 1;
+                started[FP8 ? 0 : kv] = u + 1;
             }
-            if (!ok) break;
         }
         // every copy this warp started has landed before the CTA may exit
 #pragma unroll 1
-        for (int i = 0; i < RING && i < started; ++i) {
-            const int last = i + (started - 1 - i) / RING * RING;
-            quick_wait(FP8 ? raw_full(i) : full(i), (last / RING) & 1, abort_flag, p.err, 17, false);
+        for (int kv = 0; kv < (FP8 ? 1 : 2); ++kv) {
+            const int n_st = kv ? started[1] : started[0], r = ring(kv);
+#pragma unroll 1
+            for (int i = 0; i < r && i < n_st; ++i) {
+                const int last = i + (n_st - 1 - i) / r * r;
+                quick_wait(filled(kv, i), (last / r) & 1, abort_flag, p.err, 17, false);
+            }
         }
         quick_wait(q_full, 0, abort_flag, p.err, 17, false);
     } else if (warp == W0 + 1) {
@@ -288,10 +299,11 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         bool ok = quick_wait(QCONV ? q_ready : q_full, 0, abort_flag, p.err, 7);
 #pragma unroll 1
         for (int j = 0; j < nt && ok; ++j) {
-            // K_j: 8-bit in tensor memory, 16-bit in slot 2j of the ring
-            const int b = j & 1, sk = FP8 ? 0 : (2 * j) % NS;
+            // K_j: 8-bit in tensor memory, 16-bit in its ring
+            constexpr int KR = FP8 ? 1 : KS;
+            const int b = j & 1, sk = FP8 ? 0 : j % KR;
             ok = FP8 ? quick_wait(k_full(b), (j >> 1) & 1, abort_flag, p.err, 8)
-                     : quick_wait(full(sk), (uint32_t)(2 * j / NS) & 1u, abort_flag, p.err, 8);
+                     : quick_wait(full(sk), (uint32_t)(j / KR) & 1u, abort_flag, p.err, 8);
             if (ok && j >= 2) ok = quick_wait(s_free(b), ((j >> 1) - 1) & 1, abort_flag, p.err, 12);
             if (!ok) break;
             tc_fence_after();
@@ -323,8 +335,8 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         bool ok = true;
 #pragma unroll 1
         for (int j = 0; j < nt; ++j) {
-            const int b = j & 1, u = FP8 ? j : 2 * j + 1, sv = u % NS;
-            if (!(ok = quick_wait(full(sv), (uint32_t)(u / NS) & 1u, abort_flag, p.err, 9))) break;
+            const int b = j & 1, sv = KS + j % VS;
+            if (!(ok = quick_wait(full(sv), (uint32_t)(j / VS) & 1u, abort_flag, p.err, 9))) break;
             if (!FP8 && masked(j)) {
                 const uint32_t tile = sb + L::OP + sv * L::TILE + lane * 16;
                 bool bad = false;
@@ -395,7 +407,7 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                         mbar_arrive(raw_free(rs));
                     }
                 }
-                const int u = 2 * j + 1, rs = u % RS, st = j % NS;
+                const int u = 2 * j + 1, rs = u % RS, st = j % VS;
                 if (!quick_wait(raw_full(rs), (u / RS) & 1, abort_flag, p.err, 9)) break;
                 const uint32_t src = sb + L::RAW + rs * kSeg;
                 const uint32_t dst = sb + L::OP + st * L::TILE;
@@ -403,7 +415,8 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     w[i] = lds128(src + swz128((tid >> 3) + 16 * i, tid & 7));
-                if (j >= NS && !quick_wait(free_(st), (uint32_t)(j / NS - 1) & 1u, abort_flag, p.err, 10)) break;
+                if (j >= VS && !quick_wait(free_(st), (uint32_t)(j / VS - 1) & 1u, abort_flag, p.err, 10)) break;
+                const bool look = masked(j);
                 bool bad = false;
                 const int ch = tid & 7, oc = 2 * (ch & 3), sw = ch >> 2;
 #pragma unroll
@@ -412,12 +425,12 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                     const int t = (tid >> 3) + 16 * i;
                     const uint2 h0 = widen(w[i].x), h1 = widen(w[i].y), h2 = widen(w[i].z), h3 = widen(w[i].w);
                     const uint4 a = make_uint4(h0.x, h0.y, h1.x, h1.y), b = make_uint4(h2.x, h2.y, h3.x, h3.y);
-                    bad |= nonfinite<PA_F16>(a) | nonfinite<PA_F16>(b);
+                    if (look) bad |= nonfinite<PA_F16>(a) | nonfinite<PA_F16>(b);
                     const uint32_t seg = dst + sw * kSeg;
                     sts128(seg + swz128(t, oc + sw), sw ? b : a);
                     sts128(seg + swz128(t, oc + 1 - sw), sw ? a : b);
                 }
-                if (bad && masked(j)) {                        // this thread's chunks once more
+                if (bad) {                                    // this thread's chunks once more
 #pragma unroll 1
                     for (int i = 0; i < 16; ++i) {
                         const uint32_t at = dst + sw * kSeg + swz128((tid >> 3) + 16 * (i >> 1), oc + (i & 1));
@@ -480,20 +493,27 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             if (lane == 0) mbar_arrive(s_free(b));
             const int key = kb + j * kBN + t;
             // scores in log2 units
-            float most = 0.f;
+            float most[4] = {};
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                z[r] *= QCONV ? sc[r] : p.sl;
-                if constexpr (CAP) most = fmaxf(most, fabsf(z[r]));
+            for (int r = 0; r < R; r += 2) {
+                const float2 u = mul2(make_float2(z[r], z[r + 1]),
+                                      QCONV ? make_float2(sc[r], sc[r + 1]) : make_float2(p.sl, p.sl));
+                z[r] = u.x;
+                z[r + 1] = u.y;
+                if constexpr (CAP) most[(r >> 1) & 3] = max3(most[(r >> 1) & 3], fabsf(u.x), fabsf(u.y));
             }
             if constexpr (CAP) {
                 const float cl = p.cap_log2;
-                if (!__any_sync(~0u, !(most <= 2.f))) {
+                if (!__any_sync(~0u, !(fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) <= 2.f))) {
+                    float2 co[4];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const float v = z[r] * z[r];
-                        const float y = fmaf(fmaf(fmaf(kTanh4[3], v, kTanh4[2]), v, kTanh4[1]), v, kTanh4[0]);
-                        z[r] = z[r] * cl * y;
+                    for (int k = 0; k < 4; ++k) co[k] = make_float2(kTanh4[k] * cl, kTanh4[k] * cl);
+#pragma unroll
+                    for (int r = 0; r < R; r += 2) {
+                        const float2 u = make_float2(z[r], z[r + 1]), v = mul2(u, u);
+                        const float2 y = mul2(u, fma2(fma2(fma2(co[3], v, co[2]), v, co[1]), v, co[0]));
+                        z[r] = y.x;
+                        z[r + 1] = y.y;
                     }
                 } else {
 #pragma unroll
@@ -524,17 +544,20 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                 }
             }
             // does a score exceed its row's reference by more than 8?
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float pr[R], top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int r = 0; r < R; r += 2)
-                top[(r >> 1) & 3] = max3(top[(r >> 1) & 3], z[r] + nm[r], z[r + 1] + nm[r + 1]);
+            for (int r = 0; r < R; r += 2) {
+                const float2 d = add2(make_float2(z[r], z[r + 1]), make_float2(nm[r], nm[r + 1]));
+                pr[r] = d.x;
+                pr[r + 1] = d.y;
+                top[(r >> 1) & 3] = max3(top[(r >> 1) & 3], d.x, d.y);
+            }
             const float over = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             if (__any_sync(~0u, over > kRescaleLog2 + SHIFT) && lane == 0) flags[2 * q + b] = j + 1;
             arrive();
             // the probabilities, in case no warp found one (the wait is over by then)
-            float pr[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) pr[r] = ex2(z[r] + nm[r]);
+            for (int r = 0; r < R; ++r) pr[r] = ex2(pr[r]);
             if (!(ok = joined())) break;
             if (flags[2 * q + b] == j + 1) {
                 // the tile's maxima, and everything so far against them
@@ -576,8 +599,9 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             uint32_t w[R / 2];
 #pragma unroll
             for (int r = 0; r < R; r += 2) {
-                l[r] += pr[r];
-                l[r + 1] += pr[r + 1];
+                const float2 a = add2(make_float2(l[r], l[r + 1]), make_float2(pr[r], pr[r + 1]));
+                l[r] = a.x;
+                l[r + 1] = a.y;
                 w[r / 2] = pack2<OT>(pr[r], pr[r + 1]);
             }
             if (j >= 2 && !(ok = quick_wait(pv_done(b), ((j >> 1) - 1) & 1, abort_flag, p.err, 14))) break;

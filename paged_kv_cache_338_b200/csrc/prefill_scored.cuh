@@ -526,15 +526,26 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         const uint32_t qb = sQ + (hasB ? x : 0) * L::TILE;
         int f, e;
         span(x ? rb : ra, f, e);
-        const int step = hasB ? 1 : 2, first = hasB ? 0 : x;
         // the last tile this half takes part in
         const int last = hasB ? e - 1 : nt - 1 - ((nt - 1 - x) & 1);
         bool ok = warp_wait(QCONV ? q_ready : q_full, 0, abort_flag, p.err, 7);
         int i = 0;                                             // tiles done
 #pragma unroll 1
-        for (int j = first; j < nt && ok; j += step) {
+        for (int j = 0; j < nt && ok; ++j) {
             const bool act = j >= f && j < e;
             const int sk = slot(2 * j), sv = slot(2 * j + 1);
+            if (!hasB && (j & 1) != x) {
+                // The other half's tile.  Waits go by the parity of a slot's phase, so
+                // where the halves' tiles share slots (an odd number of them) a warp has
+                // to see the phases of both: one that skips any can take an old phase
+                // for its own, and release a slot under a copy.
+                if constexpr (NS % 2)
+                    ok = warp_wait(full(sk), phase(2 * j), abort_flag, p.err, 8) &&
+                         warp_wait(full(sv), phase(2 * j + 1), abort_flag, p.err, 9);
+                else
+                    static_assert(NS % 4 == 0, "tiles 2i and 2i + 1 in slots of their own");
+                continue;
+            }
             if (!(ok = warp_wait(full(sk), phase(2 * j), abort_flag, p.err, 8))) break;
             tc_fence_after();
             if (lane == 0) {

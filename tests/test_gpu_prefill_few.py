@@ -206,3 +206,56 @@ def test_captured_replayed_and_repeated():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("L", [8, 16, 30])
+@pytest.mark.parametrize("cdt", ["bf16", "fp8"])
+def test_back_to_back_on_long_contexts(cdt, L):
+    """Launches behind each other on more CTAs than the GPU holds, each with many trips
+    round its rings (8 new tokens: the few-row kernel; 16 and 30: one query tile whose
+    halves take turns): every result the same."""
+    g = torch.Generator().manual_seed(L)
+    S, Hq, Hkv, D, bs = 12, 16, 4, 128, 16
+    n = torch.randint(2000, 24000, (S,), generator=g)
+    nblk = (n + bs - 1) // bs
+    NB = int(nblk.sum())
+    tables = torch.full((S, int(nblk.max())), -1, dtype=torch.int32)
+    at = 0
+    for s in range(S):
+        tables[s, :nblk[s]] = torch.arange(at, at + int(nblk[s]))
+        at += int(nblk[s])
+    kc, vc = (torch.randn(NB, bs, Hkv, D, device="cuda").mul_(40 if cdt == "fp8" else 1).clamp_(-448, 448)
+              .to(sc.DT[cdt]) for _ in range(2))
+    q = torch.randn(S * L, Hq, D, device="cuda").bfloat16()
+    qs = torch.arange(0, S * L + 1, L, dtype=torch.int32, device="cuda")
+    bt, cl = tables.cuda(), n.int().cuda()
+    mc = int(n.max())
+    ks = 0.025 if cdt == "fp8" else 1.0
+    first = {}
+    for rep in range(6):
+        for part in (0, 1024, 4096):
+            nb = pa.pa_prefill_scored_workspace_size(S, S * L, Hq, D, L, mc, 0, part)
+            ws = torch.empty(max(nb, 16), dtype=torch.uint8, device="cuda")
+            out = torch.empty_like(q)
+            for _ in range(4):
+                pa.pa_prefill_scored(out, q, kc, vc, bt, cl, qs, L, mc, D ** -0.5, softcap=20.0, k_scale=ks,
+                                     v_scale=ks, partition=part, workspace=ws)
+            if part not in first:
+                first[part] = out
+            assert torch.equal(out, first[part]), (rep, part)
+    assert pa.pa_device_status() == 0
+    # one sequence against its own keys, in 64 bits
+    s, h = 3, 5
+    keys = int(n[s])
+    rows = tables[s, :int(nblk[s])].long().cuda()
+    k, v = (x.view(torch.uint8)[rows].view(x.dtype).float().flatten(0, 1)[:keys, h // 4].double() * ks
+            if cdt == "fp8" else x[rows].flatten(0, 1)[:keys, h // 4].double() for x in (kc, vc))
+    z = 20.0 * torch.tanh((q[s * L:(s + 1) * L, h].double() @ k.T) * D ** -0.5 / 20.0)
+    pos = torch.arange(keys - L, keys, device="cuda")[:, None]
+    z = z.masked_fill(torch.arange(keys, device="cuda") > pos, -torch.inf)
+    want = torch.softmax(z, -1) @ v
+    bound = torch.softmax(z, -1) @ v.abs()
+    for part, out in first.items():
+        got = out[s * L:(s + 1) * L, h].double()
+        # a probability's and the output's rounding (2^-9 and 2^-9 of bf16 at most), fp32 scores
+        assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -7 + 2.0 ** -12) * bound + 1e-6).all(), part
