@@ -119,6 +119,9 @@ def test_suggested_parts():
                         p = f(S, Hq, Hkv, L, n, w)
                         assert p % 128 == 0 and p >= 0
     assert f(64, 32, 8, 2048, 8192, 0) == 0                   # enough CTAs without a split
+    assert f(16, 32, 8, 8, 1820, 0) == 0                      # short contexts
+    assert 4096 <= f(16, 32, 8, 8, 31969, 0) <= 12288
+    assert 512 <= f(1, 32, 8, 8, 9728, 0) <= 1536
     assert f(1, 32, 8, 4, 100000, 0) > 0
     with pytest.raises(pa.PaError):
         f(1, 8, 3, 1, 1, 0)
