@@ -244,19 +244,24 @@ def pa_norm_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
     any token stride, so slices of one projection output fit, and q_out may be q.
     q_weight/k_weight [D]; cos_sin fp32 [rows, rot_dim] (cosines, then sines);
     positions [T] int64; caches [NB, bs, Hkv, D]; slot_mapping [T] int64."""
-    T, Hq, D = q.shape
-    NB, bs, Hkv, _ = key_cache.shape
+    T, Hq, D = qsh = q.shape
+    csh = key_cache.shape
+    NB, bs, Hkv, Dc = csh
     kv = (T, Hkv, D)
-    strides = (_rows(q_out, (T, Hq, D), "q_out"), _rows(q, (T, Hq, D), "q"), _rows(k, kv, "k"),
-               _rows(v, kv, "v"))
+    so, sq, sk, sv = q_out.stride(), q.stride(), k.stride(), v.stride()
+    if (T > 1 and so[1:] == sq[1:] == sk[1:] == sv[1:] == (D, 1)
+            and q_out.shape == qsh and k.shape == v.shape == kv):
+        so, sq, sk, sv = so[0], sq[0], sk[0], sv[0]
+    else:                                        # sizes of 1 have any stride; or a refusal
+        so, sq, sk, sv = (_rows(q_out, qsh, "q_out"), _rows(q, qsh, "q"), _rows(k, kv, "k"),
+                          _rows(v, kv, "v"))
     in_dt = q.dtype
     if not (q_out.dtype == k.dtype == v.dtype == in_dt):
         raise PaError(1, "q_out, q, k and v must have one dtype")
     for w in (q_weight, k_weight):
         if w is not None and (w.dtype != in_dt or w.numel() != D):
             raise PaError(1, "a norm weight holds D values of the inputs' dtype")
-    if (key_cache.shape != value_cache.shape or key_cache.dtype != value_cache.dtype
-            or key_cache.shape[3] != D):
+    if csh != value_cache.shape or key_cache.dtype != value_cache.dtype or Dc != D:
         raise PaError(1, "the caches must be [NB, bs, Hkv, D] of one dtype")
     if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
         raise PaError(1, "slot_mapping must hold T int64 slots")
@@ -272,8 +277,7 @@ def pa_norm_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
     _on_current_device(q_out, q, k, v, q_weight, k_weight, cos_sin, positions, key_cache,
                        value_cache, slot_mapping)
     _check(lib().pa_norm_rope_append(
-        q_out.data_ptr(), strides[0], q.data_ptr(), strides[1], k.data_ptr(), strides[2],
-        v.data_ptr(), strides[3], _dt(q), _ptr(q_weight), _ptr(k_weight), eps, weight_offset,
+        q_out.data_ptr(), so, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, _dt(q), _ptr(q_weight), _ptr(k_weight), eps, weight_offset,
         _ptr(cos_sin), rows, _ptr(positions), rot, 1 if interleaved else 0, _ptr(key_cache),
         _ptr(value_cache), _dt(key_cache), _ptr(slot_mapping), T, Hq, Hkv, D, bs, NB, k_scale,
         v_scale, _stream(stream)))

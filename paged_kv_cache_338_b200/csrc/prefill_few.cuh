@@ -84,6 +84,7 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     constexpr int NSEG = L::NSEG, NS = L::NS, RS = L::RS, KS = L::KS, VS = L::VS;
     constexpr bool QCONV = FP8 && QT == PA_BF16;
     constexpr float SHIFT = OT == PA_F16 ? 7.f : 0.f;      // as in the kernel for many rows
+    if (threadIdx.x < 3) prefetch_tensormap(threadIdx.x == 0 ? &tmq : threadIdx.x == 1 ? &tmk : &tmv);
     grid_dependency_wait();
     const int heads = p.Hq >> p.log2G;                         // heads of a part side by side
     const int part = (int)blockIdx.x / heads, g = (int)blockIdx.x % heads;

@@ -278,6 +278,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
     constexpr int OT = FP8 ? (int)PA_F16 : QT;             // operand type
     constexpr int NSEG = L::NSEG, NS = L::NS, RS = L::RS;
     constexpr bool QCONV = FP8 && QT == PA_BF16;           // query rows brought to f16
+    if (threadIdx.x < 3) prefetch_tensormap(threadIdx.x == 0 ? &tmq : threadIdx.x == 1 ? &tmk : &tmv);
     grid_dependency_wait();
     // grid (pair slots x key parts x kv heads, sequences, pair groups): adjacent
     // pairs of one (sequence, kv head) run side by side and share K / V through
@@ -381,7 +382,14 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         dirty[1] = -1;
         fence_mbar_init();
     }
+    if (warp == 9) {
+        tmem_alloc(sb + L::MISC, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::MISC);
 
     // the halves' ranges, and which key tiles this CTA takes
     auto half = [&](int x) {
@@ -416,6 +424,8 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         }
         if (writes && p.max_parts > 1)
             p.ws_ml[out_row * p.max_parts + part] = make_float2(-INFINITY, parts == 1 && part == 0 ? -1.f : 0.f);
+        __syncthreads();
+        if (warp == 9) tmem_dealloc(tmem, kTmemCols);
         return;
     }
     // tiles [f, e) of a half hold keys its rows see; without B the halves take
@@ -443,14 +453,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         stash->maxlo = maxlo_c;
         stash->minhi = minhi_c;
     }
-    if (warp == 9) {
-        tmem_alloc(sb + L::MISC, kTmemCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::MISC);
     auto tS = [&](int x) { return tmem + 256u * x; };
     auto tO = [&](int x) { return tmem + 256u * x + 128u; };
     // use u of the operand slots (K_j: u = 2j, V_j: u = 2j + 1)
