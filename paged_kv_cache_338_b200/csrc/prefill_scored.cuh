@@ -128,33 +128,18 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return d;
 }
 
-// fma2 and mul2 that stay in the order they are written in: neighbours that share
-// an operand read it once (a packed FMA of three fresh register pairs takes 3
-// cycles, not 2).
-__device__ __forceinline__ float2 fma2_here(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm volatile("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
-        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 mul2_here(float2 a, float2 b) {
-    float2 d;
-    asm volatile("{\n\t.reg .b64 ra, rb, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 // 1 / x on the special-function unit (1 / infinity = 0).
 __device__ __forceinline__ float rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// min(a, b, c) in one instruction.
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // min(a, b), NaN if either is.
@@ -234,6 +219,20 @@ template <int DT> __device__ __forceinline__ float cache_value(const void* p, si
 // that is 1 in fp32.
 __device__ __forceinline__ float tanh_quarter(float u) {
     return fmaf(-2.f, rcp(1.f + ex2(min_nan(u * (0.5f * kLog2e), 30.f))), 1.f);
+}
+
+// The largest and the smallest of 32 values, as independent chains (NaN is passed over).
+__device__ __forceinline__ float max32(const float* s) {
+    float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+    for (int k = 4; k < 32; k += 2) m[(k >> 1) & 3] = max3(m[(k >> 1) & 3], s[k], s[k + 1]);
+    return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+__device__ __forceinline__ float min32(const float* s) {
+    float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+    for (int k = 4; k < 32; k += 2) m[(k >> 1) & 3] = min3(m[(k >> 1) & 3], s[k], s[k + 1]);
+    return fminf(min3(m[0], m[1], m[2]), m[3]);
 }
 
 // Bits a..b (inclusive, any integers) of 32-bit word g.
@@ -624,6 +623,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                 if (!warp_wait(raw_full(rs), (u / RS) & 1, abort_flag, p.err, 9)) break;
                 if (!warp_wait(free_(st), phase(u) ^ 1, abort_flag, p.err, 10)) break;
                 const uint32_t src = sRAW + rs * kSeg, dst = sOP + st * L::TILE;
+                const bool look = (u & 1) && masked(u >> 1);
                 bool bad = false;
 #pragma unroll 4
                 for (int i = tid; i < kBN * 8; i += 128) {
@@ -634,13 +634,13 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                     const uint4 w = lds128(src + swz128(t, ch));
                     const uint2 h0 = widen(w.x), h1 = widen(w.y), h2 = widen(w.z), h3 = widen(w.w);
                     const uint4 a = make_uint4(h0.x, h0.y, h1.x, h1.y), b = make_uint4(h2.x, h2.y, h3.x, h3.y);
-                    bad |= nonfinite<PA_F16>(a) | nonfinite<PA_F16>(b);
+                    if (look) bad |= nonfinite<PA_F16>(a) | nonfinite<PA_F16>(b);
                     const uint32_t seg = dst + (ch >> 2) * kSeg;
                     const int oc = 2 * (ch & 3), sw = ch >> 2;
                     sts128(seg + swz128(t, oc + sw), sw ? b : a);
                     sts128(seg + swz128(t, oc + 1 - sw), sw ? a : b);
                 }
-                if (bad && (u & 1) && masked(u >> 1)) {       // this thread's chunks once more
+                if (bad) {                                   // this thread's chunks once more
 #pragma unroll 1
                     for (int i = 0; i < 16; ++i) {
                         const int t = (tid >> 3) + 16 * (i >> 1), ch = tid & 7;
@@ -681,6 +681,9 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             if (ok) sl *= rowscale[hasB ? threadIdx.x : r];
         }
         const float slope = BIAS && row_ok ? p.slopes[hq] * kLog2e : 0.f;
+        // distances by the difference alone (no keys of a prefix ahead of a row), whose
+        // products lose nothing that matters
+        const bool linear = BIAS && !p.prefix_lens && __all_sync(~0u, fabsf(slope) <= 64.f);
         const bool live = __any_sync(~0u, row_ok);         // a warp without rows only keeps step
         // tiles [ja, jb) need no mask in this warp
         const int ja = mine.maxlo <= kb ? 0 : ((min(mine.maxlo, INT_MAX - kBN) - kb - 1) >> 7) + 1;
@@ -706,97 +709,130 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             }
             tc_fence_after();
             const bool mask = j < ja || j >= jb;
-            float sv[kBN];
-#pragma unroll
-            for (int c4 = 0; c4 < kBN / 32; ++c4) tmem_ld32(tS(x) + lrow + c4 * 32, sv + c4 * 32);
-            tmem_wait_ld();
+            const int k0 = kb + j * kBN;
             const float2 sl2 = make_float2(sl, sl);
-            // Scores in log2 units.  With a cap u = 4 scale x / softcap (the factor
-            // sl), z = cap_log2 * tanh(u / 4).  `fit`: no |u| of the warp reaches 2
-            // (the second highest bit of a float is set from 2 on, also of
-            // infinities and NaN) and no row masks: then sv keeps u, the row's
-            // maximum is tanh of the largest u, and the four-term fit runs with the
-            // exponentials below.
-            bool fit = false;
-            if constexpr (CAP) {
-                uint32_t bits[8] = {};                 // independent chains
+            const uint32_t ts = tS(x) + lrow;
+            float tmax = -INFINITY;
+            // Scores without a cap stay in registers, a row of 128.  With one the code of
+            // a tile would be three times as long, and instructions of straight code
+            // arrive at half the rate they can be issued: capped scores are worked on 32
+            // columns at a time, in rolled loops from tensor memory and back (chunked
+            // prefill, capped: 1692 -> 1497 us; without: 1257 against 1295, with a bias
+            // 1654 against 1689).
+            float sv[CAP ? 1 : kBN], s[CAP ? 32 : 1];
+            bool fit = false;              // S keeps the products, and the cap is taken below
+            if constexpr (!CAP) {
 #pragma unroll
-                for (int k = 0; k < kBN; k += 2) {
-                    const float2 u = mul2(make_float2(sv[k], sv[k + 1]), sl2);
-                    sv[k] = u.x;
-                    sv[k + 1] = u.y;
-                    bits[(k >> 1) & 7] |= __float_as_uint(u.x) | __float_as_uint(u.y);
-                }
-                const uint32_t big = ((bits[0] | bits[1] | bits[2]) | (bits[3] | bits[4] | bits[5])) | bits[6] | bits[7];
-                fit = !BIAS && !mask && !__any_sync(~0u, big & 0x40000000u);
-                if (!fit) {
-                    const float cl = p.cap_log2;
-                    float top = 0.f;
-#pragma unroll
-                    for (int k = 0; k < kBN; k += 2) top = max3(top, fabsf(sv[k]), fabsf(sv[k + 1]));
-                    if (!__any_sync(~0u, !(top <= 4.f))) {
-                        float2 co[7];
-#pragma unroll
-                        for (int t = 0; t < 7; ++t) co[t] = make_float2(kTanh7[t] * cl, kTanh7[t] * cl);
+                for (int c4 = 0; c4 < kBN / 32; ++c4) tmem_ld32(ts + c4 * 32, sv + c4 * 32);
+                tmem_wait_ld();
+                if constexpr (BIAS) {
+                    const float d0 = (float)(pos - k0);        // distance of key 0
+                    if (linear) {
+                        const float b0 = -slope * d0;
 #pragma unroll
                         for (int k = 0; k < kBN; k += 2) {
-                            const float2 u = make_float2(sv[k], sv[k + 1]);
-                            const float2 v = mul2(u, u);
-                            float2 y = co[6];
-#pragma unroll
-                            for (int t = 5; t >= 0; --t) y = fma2(y, v, co[t]);
-                            y = mul2(u, y);
-                            sv[k] = y.x;
-                            sv[k + 1] = y.y;
+                            const float2 z = fma2(make_float2(sv[k], sv[k + 1]), sl2,
+                                                  make_float2(fmaf(slope, (float)k, b0), fmaf(slope, (float)(k + 1), b0)));
+                            sv[k] = z.x;
+                            sv[k + 1] = z.y;
                         }
                     } else {
+                        // distances as exact small integers (|i - p|: keys of a prefix
+                        // ahead of the row; slopes whose products lose what matters)
 #pragma unroll
-                        for (int k = 0; k < kBN; ++k) sv[k] = cl * tanh_quarter(sv[k]);
+                        for (int k = 0; k < kBN; ++k) sv[k] = fmaf(-slope, fabsf(d0 - (float)k), sv[k] * sl);
                     }
                 }
-            }
-            if constexpr (BIAS) {
-                const float d0 = (float)(pos - (kb + j * kBN));      // distance of key 0
-                if (p.prefix_lens || fabsf(slope) > 64.f) {
-                    // distances as exact small integers (|i - p|: keys of a prefix
-                    // ahead of the row; slopes whose products lose what matters)
+                // keys outside a row's range become -inf; a tile that no row of the
+                // warp masks skips the compares
+                if (mask) {
 #pragma unroll
-                    for (int k = 0; k < kBN; ++k)
-                        sv[k] = fmaf(-slope, fabsf(d0 - (float)k), CAP ? sv[k] : sv[k] * sl);
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t bits = range_word(lo == kNoLo ? kBN : lo - k0, hi - k0, w);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!(bits & (1u << k))) sv[32 * w + k] = -INFINITY;
+                    }
+                }
+                // row maximum as 8 independent chains of three-input maxima
+                float pm[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) pm[k] = sv[k];
+#pragma unroll
+                for (int k = 8; k < kBN; k += 2) pm[(k >> 1) & 7] = max3(pm[(k >> 1) & 7], sv[k], sv[k + 1]);
+                tmax = fmaxf(max3(pm[0], pm[1], pm[2]), fmaxf(max3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])));
+                if constexpr (!BIAS) tmax *= sl;               // scale > 0
+            } else {
+                // With a cap u = 4 scale x / softcap (the factor sl), and the score is
+                // cap_log2 * tanh(u / 4) in log2 units.  `fit`: no |u| of the warp exceeds
+                // 2 and no row masks; the row's maximum is then tanh of its largest u, and
+                // the four-term fit runs with the exponentials below.  Else the modified
+                // and masked scores go back into S.
+                float lo32 = INFINITY;
+#pragma unroll 1
+                for (int c4 = 0; c4 < 4; ++c4) {
+                    tmem_ld32(ts + c4 * 32, s);
+                    tmem_wait_ld32(s);
+                    tmax = fmaxf(tmax, max32(s));
+                    lo32 = fminf(lo32, min32(s));
+                }
+                const float top = fmaxf(fabsf(tmax), fabsf(lo32)) * sl;
+                fit = !BIAS && !mask && !__any_sync(~0u, !(top <= 2.f));
+                if (fit) {
+                    tmax = p.cap_log2 * tanh_quarter(tmax * sl);
                 } else {
-                    const float b0 = -slope * d0;
+                    // modified and masked scores back into S
+                    tmax = -INFINITY;
+                    const bool small = !__any_sync(~0u, !(top <= 4.f));
+#pragma unroll 1
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        tmem_ld32(ts + c4 * 32, s);
+                        tmem_wait_ld32(s);
+                        const float cl = p.cap_log2;
+                        if (small) {
 #pragma unroll
-                    for (int k = 0; k < kBN; k += 2) {
-                        const float2 b = make_float2(fmaf(slope, (float)k, b0), fmaf(slope, (float)(k + 1), b0));
-                        const float2 z = CAP ? add2(make_float2(sv[k], sv[k + 1]), b)
-                                             : fma2(make_float2(sv[k], sv[k + 1]), sl2, b);
-                        sv[k] = z.x;
-                        sv[k + 1] = z.y;
+                            for (int k = 0; k < 32; k += 2) {
+                                const float2 u = mul2(make_float2(s[k], s[k + 1]), sl2), v = mul2(u, u);
+                                float2 y = make_float2(kTanh7[6], kTanh7[6]);
+#pragma unroll
+                                for (int t = 5; t >= 0; --t) y = fma2(y, v, make_float2(kTanh7[t], kTanh7[t]));
+                                y = mul2(mul2(u, make_float2(cl, cl)), y);
+                                s[k] = y.x;
+                                s[k + 1] = y.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) s[k] = cl * tanh_quarter(s[k] * sl);
+                        }
+                        if constexpr (BIAS) {
+                            const float d0 = (float)(pos - (k0 + c4 * 32));      // distance of the first key
+                            if (linear) {
+                                const float b0 = -slope * d0;
+#pragma unroll
+                                for (int k = 0; k < 32; k += 2) {
+                                    const float2 b = make_float2(fmaf(slope, (float)k, b0), fmaf(slope, (float)(k + 1), b0));
+                                    const float2 z = add2(make_float2(s[k], s[k + 1]), b);
+                                    s[k] = z.x;
+                                    s[k + 1] = z.y;
+                                }
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    s[k] = fmaf(-slope, fabsf(d0 - (float)k), s[k]);
+                            }
+                        }
+                        if (mask) {
+                            const uint32_t bits = range_word(lo == kNoLo ? kBN : lo - k0, hi - k0, c4);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!(bits & (1u << k))) s[k] = -INFINITY;
+                        }
+                        tmax = fmaxf(tmax, max32(s));
+                        tmem_st32(ts + c4 * 32, s);
                     }
+                    tmem_wait_st();
                 }
             }
-            // keys outside a row's range become -inf; a tile that no row of the
-            // warp masks skips the compares
-            if (mask) {
-                const int k0 = kb + j * kBN;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t bits = range_word(lo == kNoLo ? kBN : lo - k0, hi - k0, w);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!(bits & (1u << k))) sv[32 * w + k] = -INFINITY;
-                }
-            }
-            // row maximum as 8 independent chains of three-input maxima
-            float pm[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) pm[k] = sv[k];
-#pragma unroll
-            for (int k = 8; k < kBN; k += 2) pm[(k >> 1) & 7] = max3(pm[(k >> 1) & 7], sv[k], sv[k + 1]);
-            float tmax = fmaxf(max3(pm[0], pm[1], pm[2]),
-                               fmaxf(max3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-            if constexpr (!CAP && !BIAS) tmax *= sl;           // scale > 0
-            if (CAP && !BIAS && fit) tmax = p.cap_log2 * tanh_quarter(tmax);
             const float m_new = fmaxf(m_use, tmax);
             const bool raise = m_new > m_use + kRescaleLog2;
             const float alpha = raise ? ex2(m_use - m_new) : 1.f;
@@ -823,35 +859,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             // 2^15), so that small ones keep their bits; l carries the same factor.
             const float nm = (OT == PA_F16 ? 7.f : 0.f) - (m_use == -INFINITY ? 0.f : m_use);
             const float2 nm2 = make_float2(nm, nm);
-            // the fit runs on the FMA pipe beside the partner warp's exponentials
-            if (CAP && !BIAS && fit) {
-                const float cl = p.cap_log2;
-                float2 co[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) co[t] = make_float2(kTanh4[t] * cl, kTanh4[t] * cl);
-                constexpr int N = 4;                    // pairs worked on side by side
-#pragma unroll
-                for (int k = 0; k < kBN; k += 2 * N) {
-                    float2 v[N], y[N];
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        const float2 u = make_float2(sv[k + 2 * e], sv[k + 2 * e + 1]);
-                        v[e] = mul2_here(u, u);
-                    }
-#pragma unroll
-                    for (int e = 0; e < N; ++e) y[e] = fma2_here(co[3], v[e], co[2]);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) y[e] = fma2_here(y[e], v[e], co[1]);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) y[e] = fma2_here(y[e], v[e], co[0]);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        y[e] = fma2_here(make_float2(sv[k + 2 * e], sv[k + 2 * e + 1]), y[e], nm2);
-                        sv[k + 2 * e] = y[e].x;
-                        sv[k + 2 * e + 1] = y[e].y;
-                    }
-                }
-            } else if constexpr (CAP || BIAS) {
+            if constexpr (BIAS && !CAP) {
 #pragma unroll
                 for (int k = 0; k < kBN; k += 2) {
                     const float2 d = add2(make_float2(sv[k], sv[k + 1]), nm2);
@@ -862,19 +870,73 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             const int at = hasB ? j - jt : i;                  // this tile's turn
             if (x ? at >= 0 && at < nturn : at > 0 && at <= nturn)
                 if (!(ok = warp_wait(my_turn, (at - 1 + x) & 1, abort_flag, p.err, 19))) break;
+            float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+            if constexpr (!CAP) {
 #pragma unroll
-            for (int c16 = 0; c16 < kBN / 32; ++c16) {
-                uint32_t w[16];
+                for (int c16 = 0; c16 < kBN / 32; ++c16) {
+                    uint32_t w[16];
 #pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    const int k = c16 * 32 + 2 * v;
-                    float2 d = make_float2(sv[k], sv[k + 1]);
-                    if constexpr (!CAP && !BIAS) d = fma2(d, sl2, nm2);
-                    sv[k] = ex2(d.x);
-                    sv[k + 1] = ex2(d.y);
-                    w[v] = pack2<OT>(sv[k], sv[k + 1]);
+                    for (int v = 0; v < 16; ++v) {
+                        const int k = c16 * 32 + 2 * v;
+                        const float2 z = make_float2(sv[k], sv[k + 1]);
+                        const float2 d = BIAS ? z : fma2(z, sl2, nm2);
+                        sv[k] = ex2(d.x);
+                        sv[k + 1] = ex2(d.y);
+                        w[v] = pack2<OT>(sv[k], sv[k + 1]);
+                    }
+                    tmem_st16(ts + c16 * 16, w);
                 }
-                tmem_st16(tS(x) + lrow + c16 * 16, w);
+            } else {
+                // two chunks a round, the next one on its way while one is worked on
+                float s2[32];
+                auto chunk = [&](int c4, float* s, auto arg) {
+                    uint32_t w[16];
+                    arg(s);
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) {
+                        s[2 * v] = ex2(s[2 * v]);
+                        s[2 * v + 1] = ex2(s[2 * v + 1]);
+                        w[v] = pack2<OT>(s[2 * v], s[2 * v + 1]);
+                        sum[v & 1] = add2(sum[v & 1], make_float2(s[2 * v], s[2 * v + 1]));
+                    }
+                    tmem_st16(ts + c4 * 16, w);
+                };
+                auto chunks = [&](auto arg) {
+                    tmem_ld32(ts, s);
+#pragma unroll 1
+                    for (int c4 = 0; c4 < 4; c4 += 2) {
+                        tmem_wait_ld32(s);
+                        tmem_ld32(ts + c4 * 32 + 32, s2);
+                        chunk(c4, s, arg);
+                        tmem_wait_ld32(s2);
+                        if (c4 == 0) tmem_ld32(ts + 64, s);
+                        chunk(c4 + 1, s2, arg);
+                    }
+                };
+                if (!BIAS && fit) {
+                    const float cl = p.cap_log2;
+                    float2 co[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) co[t] = make_float2(kTanh4[t] * cl, kTanh4[t] * cl);
+                    chunks([&](float* s) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float2 u = mul2(make_float2(s[k], s[k + 1]), sl2), v = mul2(u, u);
+                            const float2 d = fma2(u, fma2(fma2(fma2(co[3], v, co[2]), v, co[1]), v, co[0]), nm2);
+                            s[k] = d.x;
+                            s[k + 1] = d.y;
+                        }
+                    });
+                } else {
+                    chunks([&](float* s) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float2 d = add2(make_float2(s[k], s[k + 1]), nm2);
+                            s[k] = d.x;
+                            s[k + 1] = d.y;
+                        }
+                    });
+                }
             }
             if (at >= 0 && at < nturn) {
                 __syncwarp();
@@ -883,11 +945,12 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(p_full(x));
-            // the row sum is not on the way to P.V: it is taken after the hand-off
-            float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+            // without a cap the row sum is not on the way to P.V: it is taken after the hand-off
+            if constexpr (!CAP) {
 #pragma unroll
-            for (int k = 0; k < kBN; k += 2)
-                sum[(k >> 1) & 3] = add2(sum[(k >> 1) & 3], make_float2(sv[k], sv[k + 1]));
+                for (int k = 0; k < kBN; k += 2)
+                    sum[(k >> 1) & 3] = add2(sum[(k >> 1) & 3], make_float2(sv[k], sv[k + 1]));
+            }
             lsum += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) +
                     ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
         }
