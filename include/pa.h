@@ -79,7 +79,8 @@ enum {
  * 19 prefix-records;
  * prefill: 7 q-tile, 8 k-tile-full, 9 v-tile-full, 10 k-tile-free,
  * 11 v-tile-free, 12 scores-ready, 13 probabilities-ready, 14 p.v-done,
- * 15 output-ready, 16 tensor-core drain, 17 load drain, 18 exponential turn). */
+ * 15 output-ready, 16 tensor-core drain, 17 load drain, 18 exponential turn,
+ * 20 other half's state, 21 row maxima). */
 
 /* Message for the last failing call on this thread ("" if none). */
 const char* pa_last_error(void);
@@ -155,9 +156,9 @@ pa_status pa_reshape_and_cache(const void* key, const void* value, pa_dtype in_d
  *                Both may be NULL with rot_dim == 0 (no rotation).
  *   rot_dim      a multiple of 16 in [0, D]; D in {64, 128, 256}.
  *   slot_mapping device int64 [T]; < 0: nothing is written to the cache for the
- *                token (its q row is).  Slots of one call are distinct, else
- *                one of the tokens wins.  A slot >= NB * bs writes no cache row
- *                and sets PA_DEV_BAD_SLOT.
+ *                token (its q row is).  Slots of one call are distinct; a slot
+ *                given twice ends with a mix of its tokens' rows.  A slot >=
+ *                NB * bs writes no cache row and sets PA_DEV_BAD_SLOT.
  * A position outside [0, table_rows) skips the token (q row included) and sets
  * PA_DEV_BAD_POSITION.  cache_dt == in_dt or PA_FP8_E4M3; scales as in
  * pa_reshape_and_cache.  Strides are multiples of 16 bytes, pointers 16-byte
@@ -478,6 +479,7 @@ pa_status pa_prefill(void* out, const void* q, pa_dtype q_dt, const void* key_ca
  *                are split over CTAs in parts of this many, joined by a second
  *                kernel; pa_prefill_scored_suggest_partition() gives a value for
  *                the largest sizes of a batch.
+ *   max_ctx      at most 2^30.
  *   workspace    pa_prefill_scored_workspace_size() bytes, 16-byte aligned (0 bytes
  *                needed: may be NULL); calls that overlap need one each.
  * Results with the same arguments are the same bit for bit.

@@ -462,7 +462,7 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             __syncwarp();
             if (lane == 0) mbar_arrive(sync(q));
         };
-        auto joined = [&]() { return quick_wait(sync(q), nsync++ & 1, abort_flag, p.err, 19); };
+        auto joined = [&]() { return quick_wait(sync(q), nsync++ & 1, abort_flag, p.err, 21); };
         if constexpr (QCONV) {
             ok = quick_wait(q_full, 0, abort_flag, p.err, 7);
             if (ok && t < R) {

@@ -131,6 +131,8 @@ extern "C" pa_status pa_prefill_scored(
         return fail(PA_ERR_INVALID_ARG, "scales must be finite and > 0");
     if (!fp8 && (k_scale != 1.f || v_scale != 1.f))
         return fail(PA_ERR_INVALID_ARG, "k_scale / v_scale apply to fp8 caches only");
+    // key indices past a tile's end stay within an int
+    if (max_ctx > (1 << 30)) return fail(PA_ERR_UNSUPPORTED, "max_ctx %d (2^30 at most)", max_ctx);
     if (S == 0 || T == 0 || max_query_len == 0) return PA_OK;
     if (MB == 0) return fail(PA_ERR_INVALID_ARG, "MB == 0 with new tokens");
     if (!out || !q || !key_cache || !value_cache || !block_tables || !context_lens || !query_start)

@@ -577,15 +577,18 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
 #pragma unroll 8
                     for (int v = 0; v < L::TILE; v += 512) bad |= nonfinite<OT>(lds128(tile + v));
                     if (__any_sync(~0u, bad)) {
-#pragma unroll 1
-                        for (int v = 0; v < L::TILE; v += 512) sts128(tile + v, finite_only<OT>(lds128(tile + v)));
+                        // marked first: the other warp may find the tile mended already
                         if (lane == 0) {
                             atomicMin(dirty, j);
                             atomicMax(dirty + 1, j);
+                            __threadfence_block();
                         }
-                        fence_proxy_async_smem();
                         __syncwarp();
+#pragma unroll 1
+                        for (int v = 0; v < L::TILE; v += 512) sts128(tile + v, finite_only<OT>(lds128(tile + v)));
                     }
+                    fence_proxy_async_smem();                  // this warp's mending, or what it saw of the other's
+                    __syncwarp();
                 }
                 if (!(ok = warp_wait(p_full(x), i & 1, abort_flag, p.err, 13))) break;
                 tc_fence_after();
@@ -869,7 +872,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             }
             const int at = hasB ? j - jt : i;                  // this tile's turn
             if (x ? at >= 0 && at < nturn : at > 0 && at <= nturn)
-                if (!(ok = warp_wait(my_turn, (at - 1 + x) & 1, abort_flag, p.err, 19))) break;
+                if (!(ok = warp_wait(my_turn, (at - 1 + x) & 1, abort_flag, p.err, 18))) break;
             float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
             if constexpr (!CAP) {
 #pragma unroll
@@ -965,7 +968,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                 mbar_arrive(b_done);
                 ok = false;                                // half A writes the rows
             } else if (ok && ntiles > 1) {
-                ok = warp_wait(b_done, 0, abort_flag, p.err, 18) &&
+                ok = warp_wait(b_done, 0, abort_flag, p.err, 20) &&
                      warp_wait(o_full(1), 0, abort_flag, p.err, 15);
                 const float2 b = ml_b[r];
                 const float m = fmaxf(m_use, b.x);

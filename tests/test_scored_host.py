@@ -54,6 +54,7 @@ def test_decode_refuses(kw, status):
     (dict(T=-1), INVALID), (dict(max_new=-1), INVALID), (dict(max_ctx=-1), INVALID),
     (dict(scale=-0.1), INVALID), (dict(scale=0.0), INVALID), (dict(S=70000), UNSUPPORTED),
     (dict(softcap=3e38), INVALID), (dict(q_dt=0, c_dt=0), UNSUPPORTED),
+    (dict(max_ctx=2 ** 30 + 1), UNSUPPORTED),
 ], ids=lambda x: str(x))
 def test_chunk_refuses(kw, status):
     assert call("pa_prefill_scored", CHUNK, **dict(dict(MB=40), **kw)) == status
