@@ -105,12 +105,12 @@ constexpr int kNoLo = INT_MAX, kNoHi = -1;
 
 // tanh(u / 4) = u * (c0 + c1 v + c2 v^2 + ...), v = u^2: least squares fits in v,
 // reweighted towards the smallest largest relative error.  Four terms for
-// |u| <= 2 (6e-7 in fp32 arithmetic), seven for |u| <= 4 (1.6e-7); a
-// probability is rounded to 2^-9 or 2^-12 afterwards.
+// |u| <= 2 (6e-7 in fp32 arithmetic), six for |u| <= 4 (7e-7); a probability is
+// rounded to 2^-9 or 2^-12 afterwards.  Both are smooth in u, so scores near one
+// another, the only ones that share a row's weight, are off by the same amount.
 __device__ constexpr float kTanh4[4] = {0.249999864f, -0.00520723718f, 0.00012881149f, -2.71009679e-06f};
-__device__ constexpr float kTanh7[7] = {0.249999988f, -0.00520825612f, 0.000130128946f,
-                                        -3.26275814e-06f, 7.74001316e-08f, -1.47900076e-09f,
-                                        1.55124447e-11f};
+__device__ constexpr float kTanh6[6] = {0.24999985f, -0.0052076629f, 0.00012970150f,
+                                        -3.1497602e-06f, 6.3869905e-08f, -7.3124384e-10f};
 
 // What the epilogue needs of the setup, kept in shared memory meanwhile (the
 // softmax loop needs the registers).
@@ -723,7 +723,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             // prefill, capped: 1692 -> 1497 us; without: 1257 against 1295, with a bias
             // 1654 against 1689).
             float sv[CAP ? 1 : kBN], s[CAP ? 32 : 1];
-            bool fit = false;              // S keeps the products, and the cap is taken below
+            int fit = 0;                   // terms: S keeps the products, and the cap is taken below
             if constexpr (!CAP) {
 #pragma unroll
                 for (int c4 = 0; c4 < kBN / 32; ++c4) tmem_ld32(ts + c4 * 32, sv + c4 * 32);
@@ -768,9 +768,12 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             } else {
                 // With a cap u = 4 scale x / softcap (the factor sl), and the score is
                 // cap_log2 * tanh(u / 4) in log2 units.  `fit`: no |u| of the warp exceeds
-                // 2 and no row masks; the row's maximum is then tanh of its largest u, and
-                // the four-term fit runs with the exponentials below.  Else the modified
-                // and masked scores go back into S.
+                // 2 (4) and no row masks; the row's maximum is then tanh of its largest u,
+                // and the four-term (six-term) fit runs with the exponentials below.
+                // Else the modified and masked scores go back into S.  (8 x 2048 queries of
+                // scale 3: cap 15, mostly above 2, 2110 us with the four-term fit alone and
+                // 1650 with both; caps 30 and 50, nearly all below 2, 1507 and 1497 us
+                // against 1525 and 1530, for the code that they pass over.)
                 float lo32 = INFINITY;
 #pragma unroll 1
                 for (int c4 = 0; c4 < 4; ++c4) {
@@ -780,13 +783,14 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                     lo32 = fminf(lo32, min32(s));
                 }
                 const float top = fmaxf(fabsf(tmax), fabsf(lo32)) * sl;
-                fit = !BIAS && !mask && !__any_sync(~0u, !(top <= 2.f));
+                const bool tiny = !__any_sync(~0u, !(top <= 2.f));
+                const bool small = tiny || !__any_sync(~0u, !(top <= 4.f));
+                if (!BIAS && !mask && small) fit = tiny ? 4 : 6;
                 if (fit) {
                     tmax = p.cap_log2 * tanh_quarter(tmax * sl);
                 } else {
                     // modified and masked scores back into S
                     tmax = -INFINITY;
-                    const bool small = !__any_sync(~0u, !(top <= 4.f));
 #pragma unroll 1
                     for (int c4 = 0; c4 < 4; ++c4) {
                         tmem_ld32(ts + c4 * 32, s);
@@ -796,9 +800,9 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
                                 const float2 u = mul2(make_float2(s[k], s[k + 1]), sl2), v = mul2(u, u);
-                                float2 y = make_float2(kTanh7[6], kTanh7[6]);
+                                float2 y = make_float2(kTanh6[5], kTanh6[5]);
 #pragma unroll
-                                for (int t = 5; t >= 0; --t) y = fma2(y, v, make_float2(kTanh7[t], kTanh7[t]));
+                                for (int t = 4; t >= 0; --t) y = fma2(y, v, make_float2(kTanh6[t], kTanh6[t]));
                                 y = mul2(mul2(u, make_float2(cl, cl)), y);
                                 s[k] = y.x;
                                 s[k + 1] = y.y;
@@ -916,7 +920,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                         chunk(c4 + 1, s2, arg);
                     }
                 };
-                if (!BIAS && fit) {
+                if (!BIAS && fit == 4) {
                     const float cl = p.cap_log2;
                     float2 co[4];
 #pragma unroll
@@ -926,6 +930,23 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                         for (int k = 0; k < 32; k += 2) {
                             const float2 u = mul2(make_float2(s[k], s[k + 1]), sl2), v = mul2(u, u);
                             const float2 d = fma2(u, fma2(fma2(fma2(co[3], v, co[2]), v, co[1]), v, co[0]), nm2);
+                            s[k] = d.x;
+                            s[k + 1] = d.y;
+                        }
+                    });
+                } else if (!BIAS && fit) {
+                    const float cl = p.cap_log2;
+                    float2 co[6];
+#pragma unroll
+                    for (int t = 0; t < 6; ++t) co[t] = make_float2(kTanh6[t] * cl, kTanh6[t] * cl);
+                    chunks([&](float* s) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float2 u = mul2(make_float2(s[k], s[k + 1]), sl2), v = mul2(u, u);
+                            float2 y = co[5];
+#pragma unroll
+                            for (int t = 4; t >= 0; --t) y = fma2(y, v, co[t]);
+                            const float2 d = fma2(u, y, nm2);
                             s[k] = d.x;
                             s[k + 1] = d.y;
                         }

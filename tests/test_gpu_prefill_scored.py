@@ -182,6 +182,17 @@ def test_caps_from_the_fit_to_saturation(softcap):
         sc.check(c, run(c, part), f"partition {part}", want)
 
 
+@pytest.mark.parametrize("dt,cdt,D", [("bf16", "bf16", 128), ("f16", "f16", 64), ("f16", "fp8", 128)])
+@pytest.mark.parametrize("softcap", [5.0, 12.0, 25.0])
+def test_caps_over_whole_tiles(softcap, dt, cdt, D):
+    """Products of about +-8 in most tiles of 128 keys, few of which a mask meets: with the
+    middle cap |u| = 4 z / c is at most 4 but above 2, with the others beyond and below."""
+    c = sc.make([1100, 700], [70, 129], 8, 2, D, 16, dt, cdt, softcap=softcap, seed=11)
+    want = sc.oracle(c)
+    for part in (0, 256):
+        sc.check(c, run(c, part), f"partition {part}", want)
+
+
 def test_large_and_negative_slopes():
     c = sc.make([500], [60], 4, 4, 128, 16, "bf16", "bf16", alibi=True, prefix_lens=[540], seed=4,
                 q_scale=10.0)
