@@ -248,11 +248,13 @@ def pa_norm_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
     csh = key_cache.shape
     NB, bs, Hkv, Dc = csh
     kv = (T, Hkv, D)
-    so, sq, sk, sv = q_out.stride(), q.stride(), k.stride(), v.stride()
-    if (T > 1 and so[1:] == sq[1:] == sk[1:] == sv[1:] == (D, 1)
-            and q_out.shape == qsh and k.shape == v.shape == kv):
-        so, sq, sk, sv = so[0], sq[0], sk[0], sv[0]
-    else:                                        # sizes of 1 have any stride; or a refusal
+    if q_out.shape == qsh and k.shape == v.shape == kv and T > 1:
+        (so, ho, eo), (sq, hq, eq), (sk, hk, ek), (sv, hv, ev) = (q_out.stride(), q.stride(),
+                                                                  k.stride(), v.stride())
+        packed = ho == hq == hk == hv == D and eo == eq == ek == ev == 1
+    else:
+        packed = False
+    if not packed:                               # sizes of 1 have any stride; or a refusal
         so, sq, sk, sv = (_rows(q_out, qsh, "q_out"), _rows(q, qsh, "q"), _rows(k, kv, "k"),
                           _rows(v, kv, "v"))
     in_dt = q.dtype
@@ -364,18 +366,24 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, key_cache: torch.Tensor,
 
 
 def _attention_args(out, q, key_cache, value_cache, block_tables, context_lens, slopes):
-    """The shape and dtype rules of the modified-score attentions' tensors."""
-    if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype:
+    """The shape and dtype rules of the modified-score attentions' tensors ->
+    q's shape, the caches' shape, table columns and sequences.  (A tensor's shape
+    costs 0.1 us a look, and the call of a small batch is bound by the host: each
+    is taken once.)"""
+    qsh, csh, tsh = q.shape, key_cache.shape, block_tables.shape
+    S = context_lens.numel()
+    if len(qsh) != 3 or out.shape != qsh or out.dtype != q.dtype:
         raise PaError(1, "out and q must be [rows, Hq, D] of one dtype")
-    if (key_cache.dim() != 4 or key_cache.shape != value_cache.shape
-            or key_cache.dtype != value_cache.dtype or key_cache.shape[3] != q.shape[2]):
+    if (len(csh) != 4 or csh != value_cache.shape
+            or key_cache.dtype != value_cache.dtype or csh[3] != qsh[2]):
         raise PaError(1, "the caches must be [NB, bs, Hkv, D] of one dtype")
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise PaError(1, "block_tables and context_lens must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != context_lens.numel():
+    if len(tsh) != 2 or tsh[0] != S:
         raise PaError(1, "block_tables must be [S, MB]")
-    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != q.shape[1]):
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != qsh[1]):
         raise PaError(1, "slopes must hold Hq float32 values")
+    return qsh, csh, tsh[1], S
 
 
 def pa_decode_scored_workspace_size(S: int, Hq: int, D: int, bs: int, max_ctx: int, window: int,
@@ -396,10 +404,9 @@ def pa_decode_scored(out: torch.Tensor, q: torch.Tensor, key_cache: torch.Tensor
     """pa_decode with modified scores: softcap (tanh cap, 0: none), slopes (fp32
     [Hq], distance bias), window (last keys visible, 0: all), key_start (int32
     [S], first visible key).  workspace: pa_decode_scored_workspace_size()."""
-    _attention_args(out, q, key_cache, value_cache, block_tables, context_lens, slopes)
-    S, Hq, D = q.shape
-    NB, bs, Hkv, _ = key_cache.shape
-    if context_lens.numel() != S:
+    (S, Hq, D), (NB, bs, Hkv, _), MB, lens = _attention_args(
+        out, q, key_cache, value_cache, block_tables, context_lens, slopes)
+    if lens != S:
         raise PaError(1, "context_lens must hold S lengths")
     if key_start is not None and (key_start.dtype != torch.int32 or key_start.numel() != S):
         raise PaError(1, "key_start must hold S int32 positions")
@@ -408,7 +415,7 @@ def pa_decode_scored(out: torch.Tensor, q: torch.Tensor, key_cache: torch.Tensor
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().pa_decode_scored(
         _ptr(out), _ptr(q), _dt(q), _ptr(key_cache), _ptr(value_cache), _dt(key_cache),
-        _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), S, Hq, Hkv, D, bs, NB,
+        _ptr(block_tables), MB, _ptr(context_lens), S, Hq, Hkv, D, bs, NB,
         max_ctx, scale, k_scale, v_scale, softcap, _ptr(slopes), window, _ptr(key_start),
         partition, _ptr(workspace), ws_bytes, _stream(stream)))
 
@@ -517,10 +524,8 @@ def pa_prefill_scored(out: torch.Tensor, q: torch.Tensor, key_cache: torch.Tenso
     [T], first visible key per new token), prefix_lens (int32 [S], leading keys
     every new token sees).  The cache may be fp8 (k_scale, v_scale).
     workspace: pa_prefill_scored_workspace_size()."""
-    _attention_args(out, q, key_cache, value_cache, block_tables, context_lens, slopes)
-    T, Hq, D = q.shape
-    NB, bs, Hkv, _ = key_cache.shape
-    S = context_lens.numel()
+    (T, Hq, D), (NB, bs, Hkv, _), MB, S = _attention_args(
+        out, q, key_cache, value_cache, block_tables, context_lens, slopes)
     if query_start.dtype != torch.int32 or query_start.numel() != S + 1:
         raise PaError(1, "query_start must hold S + 1 int32 offsets")
     if key_start is not None and (key_start.dtype != torch.int32 or key_start.numel() != T):
@@ -532,7 +537,7 @@ def pa_prefill_scored(out: torch.Tensor, q: torch.Tensor, key_cache: torch.Tenso
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().pa_prefill_scored(
         _ptr(out), _ptr(q), _dt(q), _ptr(key_cache), _ptr(value_cache), _dt(key_cache),
-        _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), _ptr(query_start), S, T, Hq,
+        _ptr(block_tables), MB, _ptr(context_lens), _ptr(query_start), S, T, Hq,
         Hkv, D, bs, NB, max_query_len, max_ctx, scale, k_scale, v_scale, softcap, _ptr(slopes),
         window, _ptr(key_start), _ptr(prefix_lens), partition, _ptr(workspace), ws_bytes,
         _stream(stream)))

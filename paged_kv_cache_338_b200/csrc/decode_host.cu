@@ -228,8 +228,11 @@ extern "C" pa_status pa_decode_suggest_partition(int S, int Hkv, int bs,
     for (int64_t P = 256; P < maxn; P *= 2)
         if (items(P) >= want) best = P;
     // A batch that leaves most SMs without a partition of 256 gets shorter ones (one
-    // sequence of 501 tokens, 8 kv heads, bf16: 256 tokens 22.7 us, 64 tokens 15.6).
-    while (best < maxn && best > 64 && items(best) < 148) best /= 2;
+    // sequence of 501 tokens, 8 kv heads, bf16: 256 tokens 19.0 us, 64 12.1, 32 10.7;
+    // of 200: one pass 14.3, 32 10.8; of 128: 10.9, 10.6), but 32 records a head at
+    // most from the shortest (one kv head, 4000 tokens: 64 tokens 7.4 us, 32 9.0).
+    if (maxn > 128 && items(64) < 148) best = maxn <= 1024 ? 32 : 64;
+    else while (best < maxn && best > 64 && items(best) < 148) best /= 2;
     best = (best + bs - 1) / bs * bs;
     *partition = best >= maxn ? 0 : (int)best;
     return PA_OK;

@@ -103,10 +103,11 @@ def test_workspace_sizes():
 
 def test_tiny_batches_split_further():
     f = pa.pa_decode_suggest_partition
-    assert f(8, 16, [501]) == 64
+    assert f(8, 16, [501]) == 32 and f(8, 16, [200]) == 32
+    assert f(1, 16, [1025]) == 64 and f(1, 8, [1024]) == 32   # 32 records a head from 32
     assert f(8, 16, [4000]) == 128                            # 16 x 8 partitions of 256: 128 < 148
     assert f(8, 16, [2000] * 3) == 256                        # 3 x 8 x 8 = 192
-    assert f(8, 16, [200]) == 0 and f(8, 16, [256]) == 0      # short ones stay in one pass
+    assert f(8, 16, [128]) == 0 and f(8, 16, [200] * 16) == 0 # short ones stay in one pass
     assert f(8, 16, [501] * 64) == 256 and f(32, 16, [64] * 4096) == 0
 
 
