@@ -615,6 +615,7 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             if (lane == 0) mbar_arrive(p_full(b));
         }
         // -------------------------------------------------------- epilogue
+        if (p.max_parts > 1) launch_dependents();              // the join may start launching
         const bool record = parts > 1;
         const int mine = min(rows - r0, R);                    // rows of this group (or none)
         if (ok) ok = quick_wait(pv_done((nt - 1) & 1), ((nt - 1) >> 1) & 1, abort_flag, p.err, 15);

@@ -982,6 +982,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         float fa = 1.f, fb = 0.f;                          // weights of O_X and O_B
         const bool has_o = i > 0;                          // the half's O was written
         if (ok && has_o) ok = warp_wait(o_full(x), 0, abort_flag, p.err, 15);
+        if (p.max_parts > 1) launch_dependents();              // the join may start launching
         const int ntiles = stash->nt;
         if (!hasB) {
             if (x == 1) {
@@ -1071,43 +1072,60 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
     }
 }
 
-// Join of the key parts: one warp per (new token, query head) row.
+// Join of the key parts: one warp per (new token, query head) row.  Nothing but
+// latencies bounds it: the lengths are read while the attention kernel ends (its
+// CTAs let this grid start after their own wait for the kernels before), a row's
+// maxima and sums in one load of a part a lane, and eight records at a time (4 new
+// tokens on 30000 in 17 parts, both kernels: 30.8 us before, 28.2).
 template <int QT, int D>
 __global__ void __launch_bounds__(256) prefill_scored_merge(const Params p) {
-    grid_dependency_wait();
     const int s = (int)blockIdx.y, lane = threadIdx.x & 31;
     int q0, Ls, n;
-    if (!sequence(p, s, q0, Ls, n)) return;
+    const bool good = sequence(p, s, q0, Ls, n);
+    grid_dependency_wait();
+    if (!good) return;
     const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (w >= (long long)Ls * p.Hq) return;
     const size_t row = (size_t)q0 * p.Hq + (size_t)w;
     const float2* ml = p.ws_ml + row * p.max_parts;
-    if (ml[0].y == -1.f) return;                           // written by the attention kernel
-    float m = -INFINITY;
+    float2 part = lane < p.max_parts ? ml[lane] : make_float2(-INFINITY, 0.f);
+    if (__shfl_sync(~0u, part.y, 0) == -1.f) return;       // written by the attention kernel
+    float m = part.x;
 #pragma unroll 1
-    for (int i = lane; i < p.max_parts; i += 32) m = fmaxf(m, ml[i].x);
+    for (int i = 32 + lane; i < p.max_parts; i += 32) m = fmaxf(m, ml[i].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     const float base = m == -INFINITY ? 0.f : m;
-    constexpr int E = D / 32;
+    constexpr int E = D / 32, kAhead = 8;
     float acc[E] = {}, l = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < p.max_parts; ++i) {
-        const float2 q = ml[i];
-        if (q.y == 0.f) continue;                          // no key seen: nothing was written
-        const float f = ex2(q.x - base);
-        l += q.y * f;
-        const float* o = p.ws_o + (row * p.max_parts + i) * D + lane * E;
-        if constexpr (E == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(o);
-            acc[0] = fmaf(v.x, f, acc[0]);
-            acc[1] = fmaf(v.y, f, acc[1]);
-            acc[2] = fmaf(v.z, f, acc[2]);
-            acc[3] = fmaf(v.w, f, acc[3]);
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(o);
-            acc[0] = fmaf(v.x, f, acc[0]);
-            acc[1] = fmaf(v.y, f, acc[1]);
+#pragma unroll 1
+    for (int i0 = 0; i0 < p.max_parts; i0 += kAhead) {
+        if (i0 && (i0 & 31) == 0) part = i0 + lane < p.max_parts ? ml[i0 + lane] : make_float2(-INFINITY, 0.f);
+        float sum[kAhead], v[kAhead][E];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            sum[j] = __shfl_sync(~0u, part.y, (i0 + j) & 31);
+            if (sum[j] == 0.f) continue;                   // no key seen: nothing was written
+            const float* o = p.ws_o + (row * p.max_parts + i0 + j) * D + lane * E;
+            if constexpr (E == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(o);
+                v[j][0] = x.x;
+                v[j][1] = x.y;
+                v[j][2] = x.z;
+                v[j][3] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2*>(o);
+                v[j][0] = x.x;
+                v[j][1] = x.y;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const float f = ex2(__shfl_sync(~0u, part.x, (i0 + j) & 31) - base);
+            if (sum[j] == 0.f) continue;
+            l += sum[j] * f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(v[j][e], f, acc[e]);
         }
     }
     const float inv = l == 0.f ? 0.f : p.v_scale / l;
