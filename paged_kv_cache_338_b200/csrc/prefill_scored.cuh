@@ -352,7 +352,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
         }
     }
     if (threadIdx.x == 0) {
-        const int users = hasB ? 2 : 1;                    // halves that read a slot
+        const int users = hasB ? slot_halves(NS, true) : slot_halves(NS, false);
         mbar_init(q_full, 1);
         mbar_init(q_ready, hasB ? 256 : 128);
 #pragma unroll 1
@@ -538,14 +538,15 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             const int sk = slot(2 * j), sv = slot(2 * j + 1);
             if (!hasB && (j & 1) != x) {
                 // The other half's tile.  Waits go by the parity of a slot's phase, so
-                // where the halves' tiles share slots (an odd number of them) a warp has
-                // to see the phases of both: one that skips any can take an old phase
-                // for its own, and release a slot under a copy.
-                if constexpr (NS % 2)
-                    ok = warp_wait(full(sk), phase(2 * j), abort_flag, p.err, 8) &&
-                         warp_wait(full(sv), phase(2 * j + 1), abort_flag, p.err, 9);
-                else
-                    static_assert(NS % 4 == 0, "tiles 2i and 2i + 1 in slots of their own");
+                // where the halves' tiles share slots a warp sees the phases of both, and
+                // a slot is filled again only after both have: one that skipped a phase,
+                // or looked late, would take an old one for its own.
+                if constexpr (slot_halves(NS, false) == 2) {
+                    ok = warp_wait(full(sk), phase(2 * j), abort_flag, p.err, 8);
+                    if (ok && lane == 0) mbar_arrive(free_(sk));
+                    ok = ok && warp_wait(full(sv), phase(2 * j + 1), abort_flag, p.err, 9);
+                    if (ok && lane == 0) mbar_arrive(free_(sv));
+                }
                 continue;
             }
             if (!(ok = warp_wait(full(sk), phase(2 * j), abort_flag, p.err, 8))) break;

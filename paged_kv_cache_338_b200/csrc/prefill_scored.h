@@ -10,6 +10,14 @@ namespace ps {
 
 constexpr int kPairGroup = 16;    // adjacent tile pairs scheduled side by side
 
+// Halves of a CTA of the kernel for many rows that wait for every phase of an operand
+// slot, and so take part in freeing it.  With two query tiles both halves read every
+// tile.  With one the halves take the even and the odd key tiles, K_j in slot 2j and V_j
+// in slot 2j + 1 of the ring: a number of slots that 4 divides gives each half slots of
+// its own, any other makes them share, and a half that let a slot be filled again before
+// it had looked would wait for a phase that its own tile has to bring about.
+constexpr int slot_halves(int slots, bool two_tiles) { return two_tiles || slots % 4 ? 2 : 1; }
+
 struct Params {
     void* out;
     const void* v_cache;
