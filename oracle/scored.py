@@ -2,7 +2,7 @@
 
 Plain statements from the formulas in include/pa.h, on CPU torch tensors in float64.
 They share no code with the CUDA library.  Every attention result comes with the
-two sums its error bound needs (see ``Bound``).
+sums its error bound needs (see ``Bound``).
 """
 from __future__ import annotations
 
@@ -44,26 +44,36 @@ def norm_rope(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float, weigh
 
 # ------------------------------------------------------------------------- attention
 
+LOG2E = math.log2(math.e)
+
+
+def _rounding(D: int) -> float:
+    """fp32 arithmetic of one score, relative to the sum of its terms' magnitudes: D
+    products and their sums, and the modifications, each within 2^-24."""
+    return (D + 32) * 2.0 ** -24
+
+
 @dataclasses.dataclass
 class Bound:
-    """out: the result; weighted: sum_i p_i |v_i| per output element; score: a
-    bound on how large the terms of one score get (sum_d |q_d k_d| * scale, the
-    cap, the bias), per output row."""
+    """out: the result; weighted: sum_i p_i |v_i| per output element; moved: how far
+    the output moves, to first order, where every score z_i is off by its size,
+    size_i = 1 + sum_d |q_d k_d| * scale + |what the cap leaves| + |bias| + |z_i - max z|
+    (the last for the subtraction of the maximum).  With dz_i the scores' errors,
+        d out = sum_i p_i dz_i (v_i - out),
+    at most sum_i p_i |dz_i| |v_i| + (sum_i p_i |dz_i|) * weighted: a key that weighs
+    nothing adds nothing, however large its bias."""
     out: torch.Tensor
     weighted: torch.Tensor
-    score: torch.Tensor
+    moved: torch.Tensor
 
     def tolerance(self, out_dtype: torch.dtype, p_dtype: Optional[torch.dtype], D: int):
         """How far a kernel may be off: the output's own rounding, the rounding
-        of each probability to p_dtype (in the numerator and in the sum), and the
-        fp32 arithmetic of the scores: D products and the modifications, each
-        within 2^-24 of the largest term, which move every probability by the
-        same relative amount; the weighted sum in fp32."""
+        of each probability to p_dtype (in the numerator and in the sum), the fp32
+        arithmetic of the scores, and the weighted sum in fp32."""
         half = lambda t: torch.finfo(t).eps / 2                          # noqa: E731
         up = half(p_dtype) if p_dtype is not None else 0.0
-        dz = (D + 32) * 2.0 ** -24 * (1 + self.score)
-        rel = 2 * up + 2 * dz + 2.0 ** -18
-        return half(out_dtype) * self.out.abs() + rel[..., None] * self.weighted + 1e-30
+        return (half(out_dtype) * self.out.abs() + (2 * up + 2.0 ** -18) * self.weighted
+                + _rounding(D) * self.moved + 1e-30)
 
 
 def scored_attention(q, key_cache, value_cache, block_tables, context_lens, query_start, scale,
@@ -76,7 +86,7 @@ def scored_attention(q, key_cache, value_cache, block_tables, context_lens, quer
     S = len(context_lens)
     qs = list(range(S + 1)) if query_start is None else [int(x) for x in query_start]
     out = torch.zeros(T, Hq, D, dtype=torch.float64)
-    wtd, big = torch.zeros_like(out), torch.zeros(T, Hq, dtype=torch.float64)
+    wtd, moved = torch.zeros_like(out), torch.zeros_like(out)
     qd = stored(q)
     for s in range(S):
         a, b, n = qs[s], qs[s + 1], int(context_lens[s])
@@ -103,17 +113,29 @@ def scored_attention(q, key_cache, value_cache, block_tables, context_lens, quer
         vv = stored(value_cache[blk, off]) * v_scale
         for h in range(Hq):
             z = scale * (qd[a:b, h] @ kk[:, h // G].T)
-            size = scale * (qd[a:b, h].abs() @ torch.nan_to_num(kk[:, h // G]).abs().T)
+            # (infinite elements are exact: they add no rounding)
+            q_fine, k_fine = (torch.where(torch.isfinite(x), x, 0.0).abs()
+                              for x in (qd[a:b, h], kk[:, h // G]))
+            size = abs(scale) * (q_fine @ k_fine.T)
             if softcap:
+                # an error of the product passes with the tanh's slope, largest at the
+                # end of its interval that is nearer to zero
+                near = (z.abs() - _rounding(D) * size).clamp(min=0.0) / softcap
                 z = softcap * torch.tanh(z / softcap)
-                size = size + softcap
+                size = size * (1 - torch.tanh(near) ** 2) + z.abs()
             if slopes is not None:
+                slope = abs(float(slopes[h]))
                 z = z - float(slopes[h]) * dist
-                size = size + abs(float(slopes[h])) * dist
+                # kernels may count the distance from their tile's first key, up to 128
+                # away, where that loses little (slopes up to 64 in log2 units): four
+                # roundings of it, where _rounding() has D + 32
+                size = size + slope * (dist + (4 * 128 / (D + 32) if slope * LOG2E <= 64 else 0))
             z = z.masked_fill(~seen, -math.inf)
             some = seen.any(1)
             w = torch.zeros_like(z)
             w[some] = torch.softmax(z[some], -1)
+            size = 1 + size + (z - z.amax(1, keepdim=True)).abs()
+            share = torch.where(seen & (w != 0), w * size, 0.0)
             v = vv[:, h // G]
             bad = ~torch.isfinite(v)
             if bad.any():      # a value reaches the rows that see its key, and no other
@@ -123,6 +145,7 @@ def scored_attention(q, key_cache, value_cache, block_tables, context_lens, quer
                 out[a:b, h] = fine
             else:
                 out[a:b, h] = w @ v
-            wtd[a:b, h] = w @ torch.nan_to_num(v, 0.0, 0.0, 0.0).abs()
-            big[a:b, h] = torch.where(seen, size, 0.0).amax(1)
-    return Bound(out, wtd, big)
+            v_size = torch.nan_to_num(v, 0.0, 0.0, 0.0).abs()
+            wtd[a:b, h] = w @ v_size
+            moved[a:b, h] = share @ v_size + share.sum(1, keepdim=True) * wtd[a:b, h]
+    return Bound(out, wtd, moved)
