@@ -51,7 +51,8 @@ struct FewPlan {
     static constexpr int RAW = OP + NS * TILE;
     static constexpr int P = RAW + RS * kSeg;           // 2 x 128 keys x 128 bytes
     static constexpr int META = P + 2 * kSeg;
-    // rows: lo, hi, position, slope, factor of their scores, reference, alpha, sum
+    // rows: lo, hi, position behind the cached tokens, slope, factor of their scores,
+    // reference, alpha, sum
     static constexpr int METAB = NR * 4 * 8;
     // rows of values by thread, for what goes across threads
     static constexpr int XCH = META + METAB;
@@ -147,7 +148,7 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         if (lane < NR) {
             m_lo[lane] = lo;
             m_hi[lane] = hi;
-            m_pos[lane] = (float)(c + it);
+            m_pos[lane] = (float)it;
             m_slope[lane] = BIAS && row_ok ? p.slopes[g * p.G + (lane & (p.G - 1))] * kLog2e : 0.f;
             m_scale[lane] = p.sl;
             m_nm[lane] = row_ok ? -kNoMax : kNoMax;            // rows there are not: probability 0
@@ -522,7 +523,9 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                 }
             }
             if constexpr (BIAS) {
-                const float kf = (float)key;
+                // positions counted from the first new token: a distance between numbers that
+                // fp32 holds exactly (past 2^24 it does not hold positions)
+                const float kf = (float)(key - c);
 #pragma unroll
                 for (int r = 0; r < R; r += 4) {
                     const float4 at = *reinterpret_cast<const float4*>(m_pos + r0 + r);
