@@ -262,6 +262,8 @@ pa_status pa_decode(void* out, const void* q, pa_dtype q_dt,
  *       p - i < window                           window > 0 (0: no window)
  *       i >= key_start[s]                        key_start not NULL, int32 [S]
  *
+ * A score's rounding is relative to its terms' magnitudes, whatever the cap; a cap so far
+ * above the scores that scale * k_scale / softcap leaves fp32's normal numbers is refused.
  * A sequence with no visible key (or n == 0) gives a zero row.  Blocks that
  * hold no visible key are not read, and their table entries may be anything;
  * keys and values that are not visible reach nothing, whatever they hold.

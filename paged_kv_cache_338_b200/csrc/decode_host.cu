@@ -488,7 +488,9 @@ pa_status pa::check_score_opts(const ScoreOpts& o, double scale, double k_scale,
     const bool cap = o.softcap > 0.f;
     *qk = (float)(scale * k_scale * (cap ? cap_factor / (double)o.softcap : log2e));
     *cap_log2 = cap ? (float)((double)o.softcap * log2e) : 0.f;
-    if (!std::isfinite(*qk) || !std::isfinite(*cap_log2) || (cap && !(*cap_log2 > 0.f)))
+    // (with a cap a factor below the normal numbers would have lost bits)
+    if (!std::isfinite(*qk) || !std::isfinite(*cap_log2) || (cap && !(*cap_log2 > 0.f)) ||
+        (cap && scale != 0 && !std::isnormal(*qk)))
         return fail(PA_ERR_INVALID_ARG, "scale, softcap or scale / softcap is out of range");
     return PA_OK;
 }

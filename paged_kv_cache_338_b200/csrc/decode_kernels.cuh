@@ -312,8 +312,9 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmk, const CUtensorMa
 //     z = cap_log2 * (1 - 2 / (1 + 2^x))   (cap: softcap * tanh)   or  x
 //     z -= slope * (p - i)                 (bias; slope in base-2 units, key i)
 // The quotient takes two results of the special-function unit and is within a few
-// 2^-24 of tanh absolutely, which is what the score's own rounding allows (with
-// tanhf, window_fp8 of 256 sequences: 85 us against 75 without a cap).
+// 2^-24 of tanh absolutely: that is the score's own rounding where tanh is near 1.  Below
+// |z| = softcap / 2 (x = log2 e) the score is the odd fit kTanh4, whose error goes with
+// the score, however far the cap is above it.
 struct ScoreMod {
     float cap_log2 = 0.f;
     bool bias = false;
@@ -322,10 +323,16 @@ struct ScoreMod {
 };
 
 __device__ __forceinline__ float cap_score(const ScoreMod& x, float z) {
+    // kTanh4 in x = u / (2 ln 2)
+    constexpr double t = 1.3862943611198906, t3 = t * t * t, t5 = t3 * t * t, t7 = t5 * t * t;
+    constexpr float d0 = (float)(dev::kTanh4[0] * t), d1 = (float)(dev::kTanh4[1] * t3),
+                    d2 = (float)(dev::kTanh4[2] * t5), d3 = (float)(dev::kTanh4[3] * t7);
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return fmaf(-2.f * x.cap_log2, r, x.cap_log2);
+    const float v = z * z;
+    const float y = fmaf(fmaf(fmaf(d3, v, d2), v, d1), v, d0);
+    return fabsf(z) <= kLog2e ? x.cap_log2 * y * z : fmaf(-2.f * x.cap_log2, r, x.cap_log2);
 }
 
 __device__ __forceinline__ float mod_score(const ScoreMod& x, float z, float slope, int t) {

@@ -103,12 +103,9 @@ struct Ranges {
 };
 constexpr int kNoLo = INT_MAX, kNoHi = -1;
 
-// tanh(u / 4) = u * (c0 + c1 v + c2 v^2 + ...), v = u^2: least squares fits in v,
-// reweighted towards the smallest largest relative error.  Four terms for
-// |u| <= 2 (6e-7 in fp32 arithmetic), six for |u| <= 4 (7e-7); a probability is
+// The six-term fit beside kTanh4, |u| <= 4 (7e-7 in fp32 arithmetic); a probability is
 // rounded to 2^-9 or 2^-12 afterwards.  Both are smooth in u, so scores near one
 // another, the only ones that share a row's weight, are off by the same amount.
-__device__ constexpr float kTanh4[4] = {0.249999864f, -0.00520723718f, 0.00012881149f, -2.71009679e-06f};
 __device__ constexpr float kTanh6[6] = {0.24999985f, -0.0052076629f, 0.00012970150f,
                                         -3.1497602e-06f, 6.3869905e-08f, -7.3124384e-10f};
 
