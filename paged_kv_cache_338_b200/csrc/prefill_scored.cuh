@@ -218,6 +218,22 @@ __device__ __forceinline__ float tanh_quarter(float u) {
     return fmaf(-2.f, rcp(1.f + ex2(min_nan(u * (0.5f * kLog2e), 30.f))), 1.f);
 }
 
+// cap * tanh(u / 4) by the fit of `terms` terms, as the exponentials' loops take it.
+__device__ __forceinline__ float fitted(float u, float cap, int terms) {
+    const float v = u * u;
+    float y;
+    if (terms == 4) {
+        y = kTanh4[3] * cap;
+#pragma unroll
+        for (int t = 2; t >= 0; --t) y = fmaf(y, v, kTanh4[t] * cap);
+    } else {
+        y = kTanh6[5] * cap;
+#pragma unroll
+        for (int t = 4; t >= 0; --t) y = fmaf(y, v, kTanh6[t] * cap);
+    }
+    return u * y;
+}
+
 // The largest and the smallest of 32 values, as independent chains (NaN is passed over).
 __device__ __forceinline__ float max32(const float* s) {
     float m[4] = {s[0], s[1], s[2], s[3]};
@@ -766,8 +782,10 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             } else {
                 // With a cap u = 4 scale x / softcap (the factor sl), and the score is
                 // cap_log2 * tanh(u / 4) in log2 units.  `fit`: no |u| of the warp exceeds
-                // 2 (4) and no row masks; the row's maximum is then tanh of its largest u,
-                // and the four-term (six-term) fit runs with the exponentials below.
+                // 2 (4) and no row masks; the four-term (six-term) fit then runs with the
+                // exponentials below, and the row's maximum is the same fit of its largest u
+                // (another form of the tanh would be off by 2^-23 of the cap, which for a cap
+                // of 1e9 is more than the probabilities' range).
                 // Else the modified and masked scores go back into S.  (8 x 2048 queries of
                 // scale 3: cap 15, mostly above 2, 2110 us with the four-term fit alone and
                 // 1650 with both; caps 30 and 50, nearly all below 2, 1507 and 1497 us
@@ -785,7 +803,7 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                 const bool small = tiny || !__any_sync(~0u, !(top <= 4.f));
                 if (!BIAS && !mask && small) fit = tiny ? 4 : 6;
                 if (fit) {
-                    tmax = p.cap_log2 * tanh_quarter(tmax * sl);
+                    tmax = fitted(tmax * sl, p.cap_log2, fit);
                 } else {
                     // modified and masked scores back into S
                     tmax = -INFINITY;

@@ -37,18 +37,31 @@ def test_caps_above_the_scores_decode(cap, Hq, Hkv, D, dt, cdt):
         sc.check(c, dec.run(c, part), f"cap {cap} partition {part}", want)
 
 
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("kernel", sorted(KERNELS))
+@pytest.mark.parametrize("dt,cdt,D", [("bf16", "bf16", 128), ("f16", "f16", 64), ("bf16", "fp8", 128),
+                                      ("f16", "fp8", 128)])
+def test_caps_above_the_scores_chunk(cap, kernel, dt, cdt, D):
+    c = sc.make([700, 250], KERNELS[kernel], 8, 2, D, 16, dt, cdt, softcap=cap, seed=D)
+    want = sc.oracle(c)
+    for part in (0, 256):
+        sc.check(c, chunk.run(c, part), f"cap {cap} partition {part}", want)
+
+
 @pytest.mark.parametrize("alibi", [False, True])
 @pytest.mark.parametrize("kernel", ["decode"])
 def test_small_scores_beside_capped_ones(kernel, alibi):
     """Rows of one tile from a millionth of the cap to far above it."""
-    cap = 1e5
+    cap = 1e5 if kernel == "decode" else 1e6
     if kernel == "decode":
         c = dec.decode([400] * 12, 8, 2, 128, 16, "f16", "f16", softcap=cap, alibi=alibi, seed=7)
     else:
         c = sc.make([700, 250], KERNELS[kernel], 8, 2, 128, 16, "f16", "f16", softcap=cap, alibi=alibi, seed=7)
     T = c["q"].shape[0]
-    c["q"] = (c["q"].float() * torch.logspace(-2, 4, T)[:, None, None]).clamp(-6e4, 6e4).half()
-    c["scale"] = 1000.0
+    low = -2 if kernel == "decode" else -3
+    size = torch.logspace(low, 4, T)[torch.randperm(T, generator=torch.Generator().manual_seed(7))]
+    c["q"] = (c["q"].float() * size[:, None, None]).clamp(-6e4, 6e4).half()
+    c["scale"] = cap / 100
     # keys along one direction, so that scores differ by what the small rows feel
     c["kc"] = torch.where(torch.isnan(c["kc"]), c["kc"], c["kc"] * 0.01)
     want = sc.oracle(c)
