@@ -519,7 +519,11 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                     }
                 } else {
 #pragma unroll
-                    for (int r = 0; r < R; ++r) z[r] = cl * tanh_quarter(z[r]);
+                    for (int r = 0; r < R; r += 2) {
+                        const float2 y = capped2(make_float2(z[r], z[r + 1]), cl);
+                        z[r] = y.x;
+                        z[r + 1] = y.y;
+                    }
                 }
             }
             if constexpr (BIAS) {

@@ -218,6 +218,19 @@ __device__ __forceinline__ float tanh_quarter(float u) {
     return fmaf(-2.f, rcp(1.f + ex2(min_nan(u * (0.5f * kLog2e), 30.f))), 1.f);
 }
 
+// A pair of capped scores, cap * tanh(u / 4), each by the form that is right to within
+// 7e-7 of it: kTanh4 up to |u| = 2, the special-function unit beyond.
+__device__ __forceinline__ float2 capped2(float2 u, float cap) {
+    const float2 v = mul2(u, u);
+    float2 y = make_float2(kTanh4[3], kTanh4[3]);
+#pragma unroll
+    for (int t = 2; t >= 0; --t) y = fma2(y, v, make_float2(kTanh4[t], kTanh4[t]));
+    y = mul2(y, u);
+    y.x = fabsf(u.x) <= 2.f ? y.x : tanh_quarter(u.x);
+    y.y = fabsf(u.y) <= 2.f ? y.y : tanh_quarter(u.y);
+    return mul2(y, make_float2(cap, cap));
+}
+
 // cap * tanh(u / 4) by the fit of `terms` terms, as the exponentials' loops take it.
 __device__ __forceinline__ float fitted(float u, float cap, int terms) {
     const float v = u * u;
@@ -825,7 +838,11 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                             }
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) s[k] = cl * tanh_quarter(s[k] * sl);
+                            for (int k = 0; k < 32; k += 2) {
+                                const float2 z = capped2(mul2(make_float2(s[k], s[k + 1]), sl2), cl);
+                                s[k] = z.x;
+                                s[k + 1] = z.y;
+                            }
                         }
                         if constexpr (BIAS) {
                             const float d0 = (float)(pos - (k0 + c4 * 32));      // distance of the first key

@@ -49,7 +49,7 @@ def test_caps_above_the_scores_chunk(cap, kernel, dt, cdt, D):
 
 
 @pytest.mark.parametrize("alibi", [False, True])
-@pytest.mark.parametrize("kernel", ["decode"])
+@pytest.mark.parametrize("kernel", sorted(KERNELS) + ["decode"])
 def test_small_scores_beside_capped_ones(kernel, alibi):
     """Rows of one tile from a millionth of the cap to far above it."""
     cap = 1e5 if kernel == "decode" else 1e6
