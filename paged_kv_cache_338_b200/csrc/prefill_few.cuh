@@ -13,7 +13,8 @@
 // threads.  It is not needed every tile: scores are taken against the running
 // reference m of their row, and only when one exceeds it by more than 8 (in log2
 // units; the first tile always) the rows' four warps find the tile's maxima (a warp
-// reduction a row) and rescale.  A row's sum is kept per thread and added up once.
+// reduction a row) and rescale the rows that do.  A row's sum is kept per thread and added
+// up once.
 //
 // 8-bit cache: four more warps widen the codes to f16 (exactly): K to tensor
 // memory, from where the MMA takes it as its A operand, so it does not pass
@@ -506,25 +507,22 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             }
             if constexpr (CAP) {
                 const float cl = p.cap_log2;
-                if (!__any_sync(~0u, !(fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) <= 2.f))) {
-                    float2 co[4];
+                float2 co[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) co[k] = make_float2(kTanh4[k] * cl, kTanh4[k] * cl);
+                for (int k = 0; k < 4; ++k) co[k] = make_float2(kTanh4[k] * cl, kTanh4[k] * cl);
+                // |u| <= 2: the four-term fit; beyond, the special-function unit.  What a score
+                // becomes depends on its own size alone; the vote only saves the second form.
+                auto capped = [&](auto far) {
 #pragma unroll
                     for (int r = 0; r < R; r += 2) {
                         const float2 u = make_float2(z[r], z[r + 1]), v = mul2(u, u);
                         const float2 y = mul2(u, fma2(fma2(fma2(co[3], v, co[2]), v, co[1]), v, co[0]));
-                        z[r] = y.x;
-                        z[r + 1] = y.y;
+                        z[r] = decltype(far)::value && !(fabsf(u.x) <= 2.f) ? cl * tanh_quarter(u.x) : y.x;
+                        z[r + 1] = decltype(far)::value && !(fabsf(u.y) <= 2.f) ? cl * tanh_quarter(u.y) : y.y;
                     }
-                } else {
-#pragma unroll
-                    for (int r = 0; r < R; r += 2) {
-                        const float2 y = capped2(make_float2(z[r], z[r + 1]), cl);
-                        z[r] = y.x;
-                        z[r + 1] = y.y;
-                    }
-                }
+                };
+                if (__any_sync(~0u, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) > 2.f)) capped(std::true_type());
+                else capped(std::false_type());
             }
             if constexpr (BIAS) {
                 // positions counted from the first new token: a distance between numbers that
@@ -578,9 +576,11 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                     const float4 v = *reinterpret_cast<const float4*>(xch + r * XF + lane * 4);
                     const float fresh = SHIFT - warp_max(max3(v.x, v.y, fmaxf(v.z, v.w)));
                     if (lane == 0) {
-                        // the reference of a row that sees nothing, or is not there, stays
+                        // The reference of a row that sees nothing, or is not there, stays, and
+                        // that of a row that did not ask: what another row sees is not to
+                        // change a bit of it.
                         const float old = m_nm[r0 + r];
-                        const bool raise = r0 + r < rows && fresh < old;
+                        const bool raise = r0 + r < rows && old - fresh > kRescaleLog2;
                         m_alpha[r0 + r] = raise ? ex2(fresh - old) : 1.f;
                         if (raise) m_nm[r0 + r] = fresh;
                     }

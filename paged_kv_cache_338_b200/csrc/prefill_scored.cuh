@@ -52,6 +52,7 @@
 #include <cuda_runtime.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "pa_internal.h"
 #include "prefill_scored.h"
@@ -218,17 +219,20 @@ __device__ __forceinline__ float tanh_quarter(float u) {
     return fmaf(-2.f, rcp(1.f + ex2(min_nan(u * (0.5f * kLog2e), 30.f))), 1.f);
 }
 
-// A pair of capped scores, cap * tanh(u / 4), each by the form that is right to within
-// 7e-7 of it: kTanh4 up to |u| = 2, the special-function unit beyond.
-__device__ __forceinline__ float2 capped2(float2 u, float cap) {
+// A pair of capped scores, cap * tanh(u / 4), right to within 7e-7 of each: kTanh6 up to
+// |u| = 4, the special-function unit beyond (FAR: not all of the warp's are within 4.  What
+// a score becomes does not depend on it, so neither on the scores beside it).
+template <bool FAR> __device__ __forceinline__ float2 capped2(float2 u, float cap) {
     const float2 v = mul2(u, u);
-    float2 y = make_float2(kTanh4[3], kTanh4[3]);
+    float2 y = make_float2(kTanh6[5], kTanh6[5]);
 #pragma unroll
-    for (int t = 2; t >= 0; --t) y = fma2(y, v, make_float2(kTanh4[t], kTanh4[t]));
-    y = mul2(y, u);
-    y.x = fabsf(u.x) <= 2.f ? y.x : tanh_quarter(u.x);
-    y.y = fabsf(u.y) <= 2.f ? y.y : tanh_quarter(u.y);
-    return mul2(y, make_float2(cap, cap));
+    for (int t = 4; t >= 0; --t) y = fma2(y, v, make_float2(kTanh6[t], kTanh6[t]));
+    y = mul2(mul2(u, make_float2(cap, cap)), y);
+    if constexpr (FAR) {
+        if (!(fabsf(u.x) <= 4.f)) y.x = cap * tanh_quarter(u.x);
+        if (!(fabsf(u.y) <= 4.f)) y.y = cap * tanh_quarter(u.y);
+    }
+    return y;
 }
 
 // cap * tanh(u / 4) by the fit of `terms` terms, as the exponentials' loops take it.
@@ -799,22 +803,25 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                 // exponentials below, and the row's maximum is the same fit of its largest u
                 // (another form of the tanh would be off by 2^-23 of the cap, which for a cap
                 // of 1e9 is more than the probabilities' range).
-                // Else the modified and masked scores go back into S.  (8 x 2048 queries of
+                // Else the modified and masked scores go back into S, each by its own size: on a
+                // tile that some row masks a vote would let keys that a row does not see choose
+                // its form.  (8 x 2048 queries of
                 // scale 3: cap 15, mostly above 2, 2110 us with the four-term fit alone and
                 // 1650 with both; caps 30 and 50, nearly all below 2, 1507 and 1497 us
                 // against 1525 and 1530, for the code that they pass over.)
-                float lo32 = INFINITY;
+                if (!BIAS && !mask) {
+                    float lo32 = INFINITY;
 #pragma unroll 1
-                for (int c4 = 0; c4 < 4; ++c4) {
-                    tmem_ld32(ts + c4 * 32, s);
-                    tmem_wait_ld32(s);
-                    tmax = fmaxf(tmax, max32(s));
-                    lo32 = fminf(lo32, min32(s));
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        tmem_ld32(ts + c4 * 32, s);
+                        tmem_wait_ld32(s);
+                        tmax = fmaxf(tmax, max32(s));
+                        lo32 = fminf(lo32, min32(s));
+                    }
+                    // (rows there are not have no part in the choice)
+                    const float top = row_ok ? fmaxf(fabsf(tmax), fabsf(lo32)) * sl : 0.f;
+                    fit = !__any_sync(~0u, !(top <= 2.f)) ? 4 : !__any_sync(~0u, !(top <= 4.f)) ? 6 : 0;
                 }
-                const float top = fmaxf(fabsf(tmax), fabsf(lo32)) * sl;
-                const bool tiny = !__any_sync(~0u, !(top <= 2.f));
-                const bool small = tiny || !__any_sync(~0u, !(top <= 4.f));
-                if (!BIAS && !mask && small) fit = tiny ? 4 : 6;
                 if (fit) {
                     tmax = fitted(tmax * sl, p.cap_log2, fit);
                 } else {
@@ -825,25 +832,16 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                         tmem_ld32(ts + c4 * 32, s);
                         tmem_wait_ld32(s);
                         const float cl = p.cap_log2;
-                        if (small) {
+                        auto capped = [&](auto far) {
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
-                                const float2 u = mul2(make_float2(s[k], s[k + 1]), sl2), v = mul2(u, u);
-                                float2 y = make_float2(kTanh6[5], kTanh6[5]);
-#pragma unroll
-                                for (int t = 4; t >= 0; --t) y = fma2(y, v, make_float2(kTanh6[t], kTanh6[t]));
-                                y = mul2(mul2(u, make_float2(cl, cl)), y);
-                                s[k] = y.x;
-                                s[k + 1] = y.y;
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                const float2 z = capped2(mul2(make_float2(s[k], s[k + 1]), sl2), cl);
+                                const float2 z = capped2<decltype(far)::value>(mul2(make_float2(s[k], s[k + 1]), sl2), cl);
                                 s[k] = z.x;
                                 s[k + 1] = z.y;
                             }
-                        }
+                        };
+                        if (__any_sync(~0u, fmaxf(max32(s), -min32(s)) * sl > 4.f)) capped(std::true_type());
+                        else capped(std::false_type());
                         if constexpr (BIAS) {
                             const float d0 = (float)(pos - (k0 + c4 * 32));      // distance of the first key
                             if (linear) {
