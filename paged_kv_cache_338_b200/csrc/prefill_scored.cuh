@@ -714,6 +714,8 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             ok = ok && warp_wait(q_ready, 0, abort_flag, p.err, 7);
             if (ok) sl *= rowscale[hasB ? threadIdx.x : r];
         }
+        // a factor that fp32 rounds to 0: the scores are 0, and masked ones are to stay -inf
+        sl = fmaxf(sl, __int_as_float(1));
         const float slope = BIAS && row_ok ? p.slopes[hq] * kLog2e : 0.f;
         // distances by the difference alone (no keys of a prefix ahead of a row), whose
         // products lose nothing that matters
