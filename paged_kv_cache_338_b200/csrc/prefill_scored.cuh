@@ -179,7 +179,8 @@ __device__ __forceinline__ uint2 widen(uint32_t codes) {
 }
 
 // Row r of a swizzled bf16 query tile to f16, in place, times a power of two
-// that sets its largest element to 2^14..2^15; returns the inverse.
+// that sets its largest finite element to 2^14..2^15 (infinities and NaN stay what
+// they are); returns the inverse.
 template <int D, int SEG = kSeg> __device__ __forceinline__ float row_to_f16(uint32_t tile, int r) {
     float top = 0.f;
 #pragma unroll 1
@@ -187,10 +188,11 @@ template <int D, int SEG = kSeg> __device__ __forceinline__ float row_to_f16(uin
         float f[8];
         Chunk<PA_BF16>::to_float(lds128(tile + (i >> 3) * SEG + swz128(r, i & 7)), f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]));
+        for (int k = 0; k < 8; ++k)
+            if (fabsf(f[k]) <= 3.4e38f) top = fmaxf(top, fabsf(f[k]));
     }
-    int sh = 0;                        // rows of zeros, or with an infinity: as they are
-    if (top > 0.f && top <= 3.4e38f) sh = min(126, 14 - ((int)(__float_as_uint(top) >> 23) - 127));
+    int sh = 0;                        // rows of zeros: as they are
+    if (top > 0.f) sh = min(126, 14 - ((int)(__float_as_uint(top) >> 23) - 127));
     const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
 #pragma unroll 1
     for (int i = 0; i < D / 8; ++i) {

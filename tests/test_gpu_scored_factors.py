@@ -41,3 +41,18 @@ def test_scales_below_the_normal_numbers(kernel, scale):
     want = sc.oracle(c)
     for part in (0, 128):
         sc.check(c, chunk.run(c, part), f"partition {part}", want)
+
+
+@pytest.mark.parametrize("kernel", sorted(KERNELS))
+def test_infinite_queries_on_an_8_bit_cache(kernel):
+    """A query row with an infinite and large finite elements: its scores are infinite, the cap's."""
+    c = sc.make([300, 10], KERNELS[kernel], 8, 2, 128, 16, "bf16", "fp8", softcap=3.0, seed=9)
+    codes = c["kc"].view(torch.uint8)
+    codes[..., 5] = torch.where(codes[..., 5] & 0x7F == 0, torch.full_like(codes[..., 5], 0x30), codes[..., 5])
+    c["q"][1, :, :] = 1e6
+    c["q"][1, :, 5] = float("inf")
+    c["q"][2, 3, 5] = -float("inf")
+    want = sc.oracle(c)
+    assert torch.isfinite(want.out).all()
+    for part in (0, 128):
+        sc.check(c, chunk.run(c, part), f"partition {part}", want)
