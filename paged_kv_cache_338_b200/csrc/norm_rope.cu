@@ -137,15 +137,6 @@ __device__ __forceinline__ uint2 to_e4m3x8(const float* f, float scale, float in
     return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 // The passes [lo, hi) of one kind of a token (KIND 0 queries, 1 keys, 2 values):
 // kPasses batches of loads before the first use.  A pass is ROWS heads.
 template <int IN, bool TO_FP8, int D, int KIND>

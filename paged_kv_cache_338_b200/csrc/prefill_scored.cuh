@@ -116,16 +116,6 @@ struct Stash {
     int q0, iA, g, part, parts, nt, kb, maxlo, minhi;
 };
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 // 1 / x on the special-function unit (1 / infinity = 0).
 __device__ __forceinline__ float rcp(float x) {
     float y;
