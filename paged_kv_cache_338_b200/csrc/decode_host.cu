@@ -427,9 +427,10 @@ pa_status pa::decode_impl(void* out, const void* q, pa_dtype q_dt, const void* k
         p.ws_o = reinterpret_cast<float*>(w + align16(items * sizeof(int2)) +
                                           align16(rows * sizeof(float2)));
     } else if (max_parts > 1 || force_ws || fuse) {
-        p.ws_ml = static_cast<float2*>(workspace);
-        p.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                          sizeof(float2) * (size_t)S * Hq * max_parts);
+        // rows first: they are read 16 bytes at a time, which an odd number of (m, l)
+        // in front of them would misalign
+        p.ws_o = static_cast<float*>(workspace);
+        p.ws_ml = reinterpret_cast<float2*>(p.ws_o + (size_t)S * Hq * max_parts * D);
     }
 
     L.bs = bs;

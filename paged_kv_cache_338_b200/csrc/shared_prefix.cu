@@ -171,8 +171,9 @@ extern "C" pa_status pa_decode_shared_prefix(void* out, const void* q, pa_dtype 
     const int64_t mp = parts(max_ctx, chunk, prefix_tokens);
     if (mp > 65535) return fail(PA_ERR_UNSUPPORTED, "too many partitions");
     char* w = static_cast<char*>(workspace);
-    float2* ws_ml = reinterpret_cast<float2*>(w);
-    float* ws_o = reinterpret_cast<float*>(w + sizeof(float2) * (size_t)S * Hq * mp);
+    // (the records' layout is decode_impl's)
+    float* ws_o = reinterpret_cast<float*>(w);
+    float2* ws_ml = reinterpret_cast<float2*>(ws_o + (size_t)S * Hq * mp * D);
     const size_t rec_bytes = align256((size_t)S * Hq * mp * (sizeof(float) * 2 + sizeof(float) * D));
 
     const void* k_src = key_cache;
