@@ -72,7 +72,9 @@ class Bound:
         arithmetic of the scores, and the weighted sum in fp32."""
         half = lambda t: torch.finfo(t).eps / 2                          # noqa: E731
         up = half(p_dtype) if p_dtype is not None else 0.0
-        return (half(out_dtype) * self.out.abs() + (2 * up + 2.0 ** -18) * self.weighted
+        # (below its smallest normal number a type's steps stay what they are there)
+        out = half(out_dtype) * self.out.abs().clamp(min=torch.finfo(out_dtype).smallest_normal)
+        return (out + (2 * up + 2.0 ** -18) * self.weighted
                 + _rounding(D) * self.moved + 1e-30)
 
 

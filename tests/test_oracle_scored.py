@@ -62,3 +62,13 @@ def test_infinite_keys_add_nothing_to_the_bound():
     b = sc.oracle(c)
     assert torch.isfinite(b.out).all()
     assert (b.tolerance(torch.float32, None, 128) <= 2.0 ** -10 * b.weighted).all()
+
+
+def test_subnormal_outputs_round_by_half_their_step():
+    c = sc.make([39], [1], 2, 2, 128, 16, "f16", "f16", seed=8)
+    c["vc"] = c["vc"] * 2.0 ** -22
+    want = sc.oracle(c)
+    assert (want.out.abs() < torch.finfo(torch.float16).smallest_normal).all()
+    sc.check(c, want.out.to(torch.float16), "rounded", want)
+    step = 2.0 ** -24
+    fails(c, want, want.out + 2 * step, "off by two steps")
