@@ -61,21 +61,27 @@ class Bound:
     (the last for the subtraction of the maximum).  With dz_i the scores' errors,
         d out = sum_i p_i dz_i (v_i - out),
     at most sum_i p_i |dz_i| |v_i| + (sum_i p_i |dz_i|) * weighted: a key that weighs
-    nothing adds nothing, however large its bias."""
+    nothing adds nothing, however large its bias.  spread: sum_i |v_i| over the visible
+    keys."""
     out: torch.Tensor
     weighted: torch.Tensor
     moved: torch.Tensor
+    spread: torch.Tensor
 
     def tolerance(self, out_dtype: torch.dtype, p_dtype: Optional[torch.dtype], D: int):
         """How far a kernel may be off: the output's own rounding, the rounding
         of each probability to p_dtype (in the numerator and in the sum), the fp32
-        arithmetic of the scores, and the weighted sum in fp32."""
+        arithmetic of the scores, and the weighted sum in fp32.  A probability is taken
+        against a maximum of 1, so below p_dtype's smallest normal number it is off by
+        half that number's step whatever its size (f16: 2^-25 a key; the sum is 1 at
+        least)."""
         half = lambda t: torch.finfo(t).eps / 2                          # noqa: E731
         up = half(p_dtype) if p_dtype is not None else 0.0
+        low = up * torch.finfo(p_dtype).smallest_normal if p_dtype is not None else 0.0
         # (below its smallest normal number a type's steps stay what they are there)
         out = half(out_dtype) * self.out.abs().clamp(min=torch.finfo(out_dtype).smallest_normal)
         return (out + (2 * up + 2.0 ** -18) * self.weighted
-                + _rounding(D) * self.moved + 1e-30)
+                + _rounding(D) * self.moved + low * self.spread + 1e-30)
 
 
 def scored_attention(q, key_cache, value_cache, block_tables, context_lens, query_start, scale,
@@ -88,7 +94,7 @@ def scored_attention(q, key_cache, value_cache, block_tables, context_lens, quer
     S = len(context_lens)
     qs = list(range(S + 1)) if query_start is None else [int(x) for x in query_start]
     out = torch.zeros(T, Hq, D, dtype=torch.float64)
-    wtd, moved = torch.zeros_like(out), torch.zeros_like(out)
+    wtd, moved, spread = (torch.zeros_like(out) for _ in range(3))
     qd = stored(q)
     for s in range(S):
         a, b, n = qs[s], qs[s + 1], int(context_lens[s])
@@ -149,5 +155,6 @@ def scored_attention(q, key_cache, value_cache, block_tables, context_lens, quer
                 out[a:b, h] = w @ v
             v_size = torch.nan_to_num(v, 0.0, 0.0, 0.0).abs()
             wtd[a:b, h] = w @ v_size
+            spread[a:b, h] = seen.double() @ v_size
             moved[a:b, h] = share @ v_size + share.sum(1, keepdim=True) * wtd[a:b, h]
-    return Bound(out, wtd, moved)
+    return Bound(out, wtd, moved, spread)
