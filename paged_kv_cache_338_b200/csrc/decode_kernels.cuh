@@ -598,7 +598,18 @@ struct MmaState {
     float o[NH][MD][4];                      // O^T accumulators
     float m[NH][2], l[NH][2];                // heads 2*tig, 2*tig+1 of each tile
     float slope[C::SCORED ? NH : 1][2];
+    // bf16 queries on 8-bit codes, scored: a row goes to f16 times a power of two of its
+    // own (pa_decode's takes what f16 holds of it), whose inverse is in its scores' factor
+    static constexpr bool QROW = C::SCORED && FP8 && C::QT == PA_BF16;
+    float qf[QROW ? NH : 1][2];
 };
+
+// The power of two, as its exponent, that brings the largest finite element of a row (0:
+// there is none) to 2^14..2^15.
+__device__ __forceinline__ int row_shift(float top) {
+    return top > 0.f ? min(126, 14 - ((int)(__float_as_uint(top) >> 23) - 127)) : 0;
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 template <int QT>
 __device__ __forceinline__ uint32_t to_f16x2(uint32_t w) {
@@ -639,7 +650,10 @@ __device__ __forceinline__ void mma_load_q(MmaState<C>& st, const Params& p, int
         for (int ks = 0; ks < S::KS; ++ks) {
             uint32_t b0 = 0u, b1 = 0u;
             if (head < G) {
-                if constexpr (S::FP8) {
+                if constexpr (S::QROW) {
+                    b0 = __ldg(q32 + base + ks * 8 + 2 * tig);      // converted below
+                    b1 = __ldg(q32 + base + ks * 8 + 2 * tig + 1);
+                } else if constexpr (S::FP8) {
                     // physical dims ks*16 + 4tig, +1  and  ks*16 + 4tig + 2, +3
                     b0 = to_f16x2<C::QT>(__ldg(q32 + base + ks * 8 + 2 * tig));
                     b1 = to_f16x2<C::QT>(__ldg(q32 + base + ks * 8 + 2 * tig + 1));
@@ -651,6 +665,34 @@ __device__ __forceinline__ void mma_load_q(MmaState<C>& st, const Params& p, int
             }
             st.qb[nh][ks][0] = b0;
             st.qb[nh][ks][1] = b1;
+        }
+        if constexpr (S::QROW) {
+            // four lanes hold a row
+            auto halves = [](uint32_t w) { return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
+            float top = 0.f;
+            #pragma unroll
+            for (int ks = 0; ks < S::KS; ++ks)
+                #pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 f = halves(st.qb[nh][ks][k]);
+                    if (fabsf(f.x) <= 3.4e38f) top = fmaxf(top, fabsf(f.x));
+                    if (fabsf(f.y) <= 3.4e38f) top = fmaxf(top, fabsf(f.y));
+                }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int sh = row_shift(top);
+            const float up = power_of_two(sh);
+            #pragma unroll
+            for (int ks = 0; ks < S::KS; ++ks)
+                #pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 f = halves(st.qb[nh][ks][k]);
+                    __half2 h = __floats2half2_rn(f.x * up, f.y * up);
+                    st.qb[nh][ks][k] = *reinterpret_cast<uint32_t*>(&h);
+                }
+            const float inv = power_of_two(-sh) * p.qk_scale;
+            #pragma unroll
+            for (int j = 0; j < 2; ++j) st.qf[nh][j] = __shfl_sync(0xffffffffu, inv, (2 * tig + j) * 4);
         }
         #pragma unroll
         for (int md = 0; md < S::MD; ++md)
@@ -777,7 +819,7 @@ __device__ __forceinline__ void mma_block(MmaState<C>& st, uint8_t* ktile_p, uin
             #pragma unroll
             for (int nh = 0; nh < S::NH; ++nh)
                 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[mt][nh][i] *= qk_scale;
+                for (int i = 0; i < 4; ++i) sc[mt][nh][i] *= S::QROW ? st.qf[nh][i & 1] : qk_scale;
         if (mod.cap_log2 > 0.f) {
             #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
