@@ -322,23 +322,38 @@ struct ScoreMod {
     int dist0 = 0;     // distance of the query to the stage's token 0
 };
 
-__device__ __forceinline__ float cap_score(const ScoreMod& x, float z) {
+template <bool FAR>
+__device__ __forceinline__ float cap_score(float cap, float z) {
     // kTanh4 in x = u / (2 ln 2)
     constexpr double t = 1.3862943611198906, t3 = t * t * t, t5 = t3 * t * t, t7 = t5 * t * t;
     constexpr float d0 = (float)(dev::kTanh4[0] * t), d1 = (float)(dev::kTanh4[1] * t3),
                     d2 = (float)(dev::kTanh4[2] * t5), d3 = (float)(dev::kTanh4[3] * t7);
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     const float v = z * z;
-    const float y = fmaf(fmaf(fmaf(d3, v, d2), v, d1), v, d0);
-    return fabsf(z) <= kLog2e ? x.cap_log2 * y * z : fmaf(-2.f * x.cap_log2, r, x.cap_log2);
+    const float y = cap * fmaf(fmaf(fmaf(d3, v, d2), v, d1), v, d0) * z;
+    if constexpr (FAR) {
+        float e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+        return fabsf(z) <= kLog2e ? y : fmaf(-2.f * cap, r, cap);
+    }
+    return y;
 }
 
-__device__ __forceinline__ float mod_score(const ScoreMod& x, float z, float slope, int t) {
-    if (x.cap_log2 > 0.f) z = cap_score(x, z);
-    if (x.bias) z = fmaf(-slope, (float)(x.dist0 - t), z);
-    return z;
+// The N scores a lane holds.  Whether a warp computes the quotient at all goes by a vote;
+// what a score becomes goes by its own size (heads of 128, fp32 caches, 64 sequences with
+// scores mostly below half the cap: 712 us with both forms always, 486 with the vote).
+template <int N>
+__device__ __forceinline__ void cap_scores(float cap, float* z) {
+    float top = 0.f;
+    #pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(z[i]));
+    if (__any_sync(0xffffffffu, top > kLog2e)) {
+        #pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = cap_score<true>(cap, z[i]);
+    } else {
+        #pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = cap_score<false>(cap, z[i]);
+    }
 }
 
 // The stage whose token 0 is token t0 of the sequence (n tokens, first visible lo).
@@ -427,10 +442,21 @@ __device__ __forceinline__ void simt_block(SimtState<C>& st, const uint8_t* ktil
                 a += __shfl_xor_sync(0xffffffffu, a, 1);
                 a += __shfl_xor_sync(0xffffffffu, a, 2);
                 a += __shfl_xor_sync(0xffffffffu, a, 4);
-                if constexpr (C::SCORED)
-                    sc[it][g] = t < nvalid && t >= mod.first ? mod_score(mod, a, st.slope[g], t)
-                                                             : -INFINITY;
+                if constexpr (C::SCORED) sc[it][g] = a;       // modified and masked below
                 else sc[it][g] = (t < nvalid) ? a : -INFINITY;
+            }
+        }
+        if constexpr (C::SCORED) {
+            if (mod.cap_log2 > 0.f) cap_scores<IT * C::GC>(mod.cap_log2, &sc[0][0]);
+            #pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                const int t = sb * SUB + it * 4 + grp;
+                const bool seen = t < nvalid && t >= mod.first;
+                #pragma unroll
+                for (int g = 0; g < C::GC; ++g) {
+                    if (mod.bias) sc[it][g] = fmaf(-st.slope[g], (float)(mod.dist0 - t), sc[it][g]);
+                    if (!seen) sc[it][g] = -INFINITY;
+                }
             }
         }
         #pragma unroll
@@ -820,14 +846,7 @@ __device__ __forceinline__ void mma_block(MmaState<C>& st, uint8_t* ktile_p, uin
             for (int nh = 0; nh < S::NH; ++nh)
                 #pragma unroll
                 for (int i = 0; i < 4; ++i) sc[mt][nh][i] *= S::QROW ? st.qf[nh][i & 1] : qk_scale;
-        if (mod.cap_log2 > 0.f) {
-            #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                #pragma unroll
-                for (int nh = 0; nh < S::NH; ++nh)
-                    #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[mt][nh][i] = cap_score(mod, sc[mt][nh][i]);
-        }
+        if (mod.cap_log2 > 0.f) cap_scores<MT * S::NH * 4>(mod.cap_log2, &sc[0][0][0]);
         if (mod.bias) {
             #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
