@@ -143,7 +143,8 @@ pa_status pa_reshape_and_cache(const void* key, const void* value, pa_dtype in_d
  *       slot_mapping[t] of key_cache / value_cache, as pa_reshape_and_cache
  *       writes them (fp8: y / k_scale, v / v_scale to nearest even, saturating).
  *
- * All arithmetic is fp32 and each result is rounded once, to nearest even.
+ * All arithmetic is fp32 (squares are summed in it: rows up to about 10^18) and
+ * each result is rounded once, to nearest even.
  *
  *   q, q_out     [T, Hq, D] of in_dt (F32, F16, BF16): D contiguous, heads D
  *                apart, tokens q_stride / q_out_stride ELEMENTS apart (so the
@@ -206,7 +207,11 @@ pa_status pa_decode_workspace_size(int S, int Hq, int D, int max_ctx, int partit
 
 /*
  * Split size pa_decode would pick for this batch to fill the GPU: a multiple
- * of bs, or 0 for a single pass.  Host-only heuristic, no device access.
+ * of bs, or 0 for a single pass.  Host-only heuristic, no device access.  Small
+ * batches of short sequences get small partitions (32 tokens at the least), and
+ * grid and workspace grow with max_ctx / partition: a caller that keeps the
+ * value for a larger max_ctx (a captured step whose sequences grow) passes the
+ * lengths that they are to reach.
  */
 pa_status pa_decode_suggest_partition(int S, int Hkv, int bs, const int32_t* context_lens_host,
                                       int* partition);
@@ -257,13 +262,16 @@ pa_status pa_decode(void* out, const void* q, pa_dtype q_dt,
  *
  *   z_i = scale * <q[s, h, :], k_i>
  *   z_i = softcap * tanh(z_i / softcap)          softcap > 0 (0: none)
- *   z_i = z_i - slopes[h] * (p - i)              slopes not NULL, fp32 [Hq]
+ *   z_i = z_i - slopes[h] * (p - i)              slopes not NULL, fp32 [Hq], below 2^125
  *   out[s, h, :] = sum_i softmax(z)_i v_i over the visible keys, those with
  *       p - i < window                           window > 0 (0: no window)
  *       i >= key_start[s]                        key_start not NULL, int32 [S]
  *
  * A score's rounding is relative to its terms' magnitudes, whatever the cap; a cap so far
  * above the scores that scale * k_scale / softcap leaves fp32's normal numbers is refused.
+ * On a tensor-core consumer probabilities are rounded to the type of its products (the
+ * 16-bit cache's, f16 for fp8), as in pa_decode; bf16 queries on an fp8 cache may be of
+ * any size (pa_decode takes them in f16: up to 65504).
  * A sequence with no visible key (or n == 0) gives a zero row.  Blocks that
  * hold no visible key are not read, and their table entries may be anything;
  * keys and values that are not visible reach nothing, whatever they hold.
@@ -454,7 +462,7 @@ pa_status pa_prefill(void* out, const void* q, pa_dtype q_dt, const void* key_ca
  *
  *   z_i = scale * <q[t, h, :], k_i>
  *   z_i = softcap * tanh(z_i / softcap)          softcap > 0 (0: none)
- *   z_i = z_i - slopes[h] * |i - p|              slopes not NULL, fp32 [Hq]
+ *   z_i = z_i - slopes[h] * |i - p|              slopes not NULL, fp32 [Hq], below 2^125
  *   out[t, h, :] = sum_i softmax(z)_i v_i over the visible keys, those with
  *       i <= p, or i < prefix_lens[s]            prefix_lens not NULL, int32 [S]:
  *                                                leading keys every new token sees
@@ -484,7 +492,8 @@ pa_status pa_prefill(void* out, const void* q, pa_dtype q_dt, const void* key_ca
  *   max_ctx      at most 2^30.
  *   workspace    pa_prefill_scored_workspace_size() bytes, 16-byte aligned (0 bytes
  *                needed: may be NULL); calls that overlap need one each.
- * Results with the same arguments are the same bit for bit.
+ * Results with the same arguments are the same bit for bit, and no bit of a row depends
+ * on keys that the row does not see.
  */
 pa_status pa_prefill_scored_suggest_partition(int S, int Hq, int Hkv, int max_query_len,
                                               int max_ctx, int window, int* partition);

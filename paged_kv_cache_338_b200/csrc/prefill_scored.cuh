@@ -32,6 +32,11 @@
 // element 2^-29 of that and smaller loses bits, below fp32's own rounding of
 // the sum), and its inverse multiplies the row's scores.
 //
+// Rounding.  Scores, maxima, sums and O are fp32.  Probabilities are rounded to the operand
+// type, half a step (2^-9 of bf16, 2^-12 of f16) each: the MMA takes both operands in one
+// type, V is stored in it, and together the errors come to about what the output's own
+// rounding adds.  The row's sum takes them unrounded, off the way to P.V.
+//
 // Not-a-numbers.  A probability of zero times a non-finite value is no zero, so
 // where a row does not see a key, that key's value must not meet the row in the
 // product.  In tiles that some row masks, a warp looks through V (one multiply
@@ -745,8 +750,8 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
             // a tile would be three times as long, and instructions of straight code
             // arrive at half the rate they can be issued: capped scores are worked on 32
             // columns at a time, in rolled loops from tensor memory and back (chunked
-            // prefill, capped: 1692 -> 1497 us; without: 1257 against 1295, with a bias
-            // 1654 against 1689).
+            // prefill, capped: 1692 -> 1497 us, 1537 with all that came later; without: 1257
+            // against 1295, with a bias 1654 against 1689).
             float sv[CAP ? 1 : kBN], s[CAP ? 32 : 1];
             int fit = 0;                   // terms: S keeps the products, and the cap is taken below
             if constexpr (!CAP) {
@@ -802,7 +807,9 @@ prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq,
                 // its form.  (8 x 2048 queries of
                 // scale 3: cap 15, mostly above 2, 2110 us with the four-term fit alone and
                 // 1650 with both; caps 30 and 50, nearly all below 2, 1507 and 1497 us
-                // against 1525 and 1530, for the code that they pass over.)
+                // against 1525 and 1530, for the code that they pass over.  A score's own
+                // size in place of the vote on masked tiles: 1684, 1530 and 1537; cap 10,
+                // mostly above 4, 2748 -> 2933.)
                 if (!BIAS && !mask) {
                     float lo32 = INFINITY;
 #pragma unroll 1
